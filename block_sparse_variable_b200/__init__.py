@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
 
@@ -87,10 +88,19 @@ def _load():
     lib.bsa_selftest_e4m3.argtypes = [vp, vp, ctypes.c_int64, vp]
     lib.bsa_selftest_wait_timeout.argtypes = [vp, vp]
     lib.bsa_selftest_f32x2.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int64, vp]
+    i64 = ctypes.c_int64
+    lib.bsa_block_means_get_workspace.argtypes = [vp] * 7 + [sz]
+    lib.bsa_block_means.argtypes = [vp] * 7 + [vp, s_t, vp]
+    lib.bsa_select_blocks_get_workspace.argtypes = [vp] * 6 + [i64, i64, vp, sz]
+    lib.bsa_select_blocks.argtypes = [vp] * 6 + [i64, i64, vp, vp, s_t, vp]
+    lib.bsa_decode_get_workspace.argtypes = [vp] * 12 + [sz]
+    lib.bsa_decode.argtypes = [vp] * 12 + [vp, s_t, vp]
     for f in ("bsa_fwd_get_workspace", "bsa_fwd", "bsa_fwd_workspace_layout",
               "bsa_bwd_get_workspace", "bsa_bwd", "bsa_bwd_workspace_layout", "bsa_read_status",
               "bsa_set_main_kernel_events", "bsa_selftest_exp2", "bsa_selftest_wait_timeout",
-              "bsa_selftest_e4m3", "bsa_selftest_f32x2"):
+              "bsa_selftest_e4m3", "bsa_selftest_f32x2", "bsa_block_means_get_workspace",
+              "bsa_block_means", "bsa_select_blocks_get_workspace", "bsa_select_blocks",
+              "bsa_decode_get_workspace", "bsa_decode"):
         getattr(lib, f).restype = ctypes.c_int
     return lib
 
@@ -101,7 +111,9 @@ EXPORTED = ("bsa_fwd_get_workspace", "bsa_fwd", "bsa_bwd_get_workspace", "bsa_bw
             "bsa_read_status", "bsa_status_string", "bsa_fwd_workspace_layout",
             "bsa_bwd_workspace_layout", "bsa_abi_version", "bsa_fwd_static_workspace",
             "bsa_set_main_kernel_events", "bsa_selftest_exp2", "bsa_selftest_wait_timeout",
-            "bsa_selftest_e4m3", "bsa_selftest_f32x2")
+            "bsa_selftest_e4m3", "bsa_selftest_f32x2", "bsa_block_means_get_workspace",
+            "bsa_block_means", "bsa_select_blocks_get_workspace", "bsa_select_blocks",
+            "bsa_decode_get_workspace", "bsa_decode")
 
 
 def lib():
@@ -405,3 +417,175 @@ def bsa_fwd_static_workspace(q, k, v, index, params: Params, *, cu_seqlens_q=Non
     _check(f(*[_ref(x) for x in ins], ctypes.byref(cp), _ref(o), _ref(l),
              ctypes.c_void_p(_stream(stream))), "bsa_fwd_static_workspace")
     return out, lse
+
+
+# ---------------------------------------------------------- cache operators
+# A decoding step makes one call for a few microseconds of GPU work, so these
+# marshal all descriptors of a call into one buffer.
+_TENSOR = struct.Struct("Qii4q4q")  # bsa_tensor
+_PARAMS = struct.Struct("iiqqqqdiiii")  # bsa_params, padded to its alignment
+assert _TENSOR.size == ctypes.sizeof(bsa_tensor) and _PARAMS.size == ctypes.sizeof(bsa_params)
+_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+
+
+def _marshal(params: Params, tensors):
+    """(buffer, address of the bsa_params, addresses of the tensors, None for
+    the absent); the addresses hold while the buffer does."""
+    buf = ctypes.create_string_buffer(_PARAMS.size + _TENSOR.size * len(tensors))
+    base = ctypes.addressof(buf)
+    p = params
+    _PARAMS.pack_into(buf, 0, LAYOUTS[p.q_layout], LAYOUTS[p.kv_layout], p.num_heads, p.num_kv_heads,
+                      p.block_shape[0], p.block_shape[1], p.scale, 1 if p.return_lse else 0,
+                      1 if p.causal else 0, 1 if p.deterministic else 0, 0)
+    at, refs = _PARAMS.size, []
+    for t in tensors:
+        if t is None:
+            refs.append(None)
+            continue
+        n = t.dim()
+        if n > 4:
+            raise ValueError("at most 4 dimensions")
+        pad = _PAD[n]
+        _TENSOR.pack_into(buf, at, t.data_ptr() or (_EMPTY_PTR if t.numel() == 0 else 0),
+                          _DTYPES.get(t.dtype, 0), n, *t.shape, *pad, *t.stride(), *pad)
+        refs.append(base + at)
+        at += _TENSOR.size
+    return buf, base, refs
+
+
+def _run_on(dev: int, workspace, size, call, stream, where, tensors):
+    """Checks devices, finds the workspace (`size()` bytes when the caller has
+    none) and makes `call(workspace, bytes, stream)` on the tensors' device."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: all tensors must be on one CUDA device")
+    if dev < 0:
+        raise ValueError(f"{where}: the tensors must be on a CUDA device")
+    if workspace is None:
+        workspace = torch.empty(max(size(), 256), dtype=torch.uint8, device=tensors[0].device)
+    elif workspace.get_device() != dev:
+        raise ValueError(f"{where}: the workspace must be on the tensors' device")
+    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    n = workspace.numel() * workspace.element_size()
+    if torch.cuda.current_device() == dev:
+        st = call(workspace.data_ptr(), n, s)
+    else:
+        with torch.cuda.device(dev):
+            st = call(workspace.data_ptr(), n, s)
+    _check(st, where)
+    return workspace
+
+
+def _means_size(refs, prm) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.bsa_block_means_get_workspace(*refs[:5], prm, refs[5], ctypes.byref(n)),
+           "bsa_block_means_get_workspace")
+    return n.value
+
+
+def bsa_block_means_get_workspace(k, means, params: Params, *, cu_seqlens_kv=None, seqused_kv=None,
+                                  block_table=None, first_kv=None) -> int:
+    buf, prm, refs = _marshal(params, (k, cu_seqlens_kv, seqused_kv, block_table, first_kv, means))
+    return _means_size(refs, prm)
+
+
+def bsa_block_means(k, params: Params, *, cu_seqlens_kv=None, seqused_kv=None, block_table=None,
+                    first_kv=None, means=None, workspace=None, stream=None):
+    """Means of the keys of every kv block (from token first_kv[b] on), into
+    `means` [B, N2, NB, D].  Without `means` a zeroed tensor is made with room
+    for every block the cache can hold.  Returns (means, workspace)."""
+    if means is None:
+        N2, bkv = params.num_kv_heads or params.num_heads, params.block_shape[1]
+        if params.kv_layout == "TND":
+            B, most = cu_seqlens_kv.shape[0] - 1, k.shape[0]
+        elif params.kv_layout == "PA_BBND":
+            B, most = block_table.shape[0], block_table.shape[1] * k.shape[1]
+        else:
+            B, most = k.shape[0], k.shape[2]
+        means = torch.zeros(B, N2, -(-most // bkv), k.shape[-1], dtype=k.dtype, device=k.device)
+    tensors = (k, cu_seqlens_kv, seqused_kv, block_table, first_kv, means)
+    buf, prm, refs = _marshal(params, tensors)
+    workspace = _run_on(k.get_device(), workspace, lambda: _means_size(refs, prm),
+                        lambda w, n, s: _lib.bsa_block_means(*refs[:5], prm, refs[5], w, n, s),
+                        stream, "bsa_block_means", tensors)
+    return means, workspace
+
+
+def _select_size(refs, prm, sink, local) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.bsa_select_blocks_get_workspace(*refs[:5], prm, sink, local, refs[5], ctypes.byref(n)),
+           "bsa_select_blocks_get_workspace")
+    return n.value
+
+
+def bsa_select_blocks_get_workspace(q, means, index, params: Params, *, sink_blocks=0, local_blocks=0,
+                                    cu_seqlens_q=None, cu_seqlens_kv=None, seqused_kv=None) -> int:
+    buf, prm, refs = _marshal(params, (q, means, cu_seqlens_q, cu_seqlens_kv, seqused_kv, index))
+    return _select_size(refs, prm, int(sink_blocks), int(local_blocks))
+
+
+def bsa_select_blocks(q, means, params: Params, *, width=None, index_heads=None, rows=None,
+                      sink_blocks=0, local_blocks=0, cu_seqlens_q=None, cu_seqlens_kv=None,
+                      seqused_kv=None, index=None, workspace=None, stream=None):
+    """The block index of bsa_fwd / bsa_bwd / bsa_decode: for every query
+    block the blocks of the highest q . means score.  Without `index` one is
+    made with `width` slots, `index_heads` heads (default: one row per kv
+    head) and, for TND queries, `rows` rows (the sum of ceil(qlen /
+    block_shape[0]); by default an upper bound, whose last rows are then
+    unused 0xFFFF).  Returns (index, workspace)."""
+    if index is None:
+        if width is None:
+            raise ValueError("bsa_select_blocks: width or index")
+        H = index_heads or params.num_kv_heads or params.num_heads
+        bq = params.block_shape[0]
+        if params.q_layout == "BNSD":
+            index = torch.empty(q.shape[0], H, -(-q.shape[2] // bq), width, dtype=torch.uint16, device=q.device)
+        elif rows is not None:
+            index = torch.empty(H, rows, width, dtype=torch.uint16, device=q.device)
+        else:
+            B = cu_seqlens_q.shape[0] - 1
+            most = min(q.shape[0], q.shape[0] // bq + B)
+            index = torch.full((H, most, width), -1, dtype=torch.int16, device=q.device).view(torch.uint16)
+    sink, local = int(sink_blocks), int(local_blocks)
+    tensors = (q, means, cu_seqlens_q, cu_seqlens_kv, seqused_kv, index)
+    buf, prm, refs = _marshal(params, tensors)
+    workspace = _run_on(q.get_device(), workspace, lambda: _select_size(refs, prm, sink, local),
+                        lambda w, n, s: _lib.bsa_select_blocks(*refs[:5], prm, sink, local, refs[5], w, n, s),
+                        stream, "bsa_select_blocks", tensors)
+    return index, workspace
+
+
+def _decode_size(refs, prm) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.bsa_decode_get_workspace(*refs[:9], prm, refs[9], refs[10], ctypes.byref(n)),
+           "bsa_decode_get_workspace")
+    return n.value
+
+
+def bsa_decode_get_workspace(q, k, v, params: Params, *, index=None, tree_mask=None, cu_seqlens_q=None,
+                             cu_seqlens_kv=None, seqused_kv=None, block_table=None, out=None,
+                             lse=None) -> int:
+    out = q if out is None else out
+    if lse is None and params.return_lse:
+        lse = torch.empty(_lse_shape(q, params), dtype=torch.float32)
+    buf, prm, refs = _marshal(params, (q, k, v, index, tree_mask, cu_seqlens_q, cu_seqlens_kv,
+                                       seqused_kv, block_table, out, lse))
+    return _decode_size(refs, prm)
+
+
+def bsa_decode(q, k, v, params: Params, *, index=None, tree_mask=None, cu_seqlens_q=None,
+               cu_seqlens_kv=None, seqused_kv=None, block_table=None, out=None, lse=None,
+               workspace=None, stream=None):
+    """Attention of a few query tokens per sequence over the whole cache or the
+    blocks of `index`, with no mask, the causal mask or the ancestor bits of a
+    draft tree.  Returns (out, lse, workspace)."""
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and params.return_lse:
+        lse = torch.empty(_lse_shape(q, params), dtype=torch.float32, device=q.device)
+    tensors = (q, k, v, index, tree_mask, cu_seqlens_q, cu_seqlens_kv, seqused_kv, block_table, out, lse)
+    buf, prm, refs = _marshal(params, tensors)
+    workspace = _run_on(q.get_device(), workspace, lambda: _decode_size(refs, prm),
+                        lambda w, n, s: _lib.bsa_decode(*refs[:9], prm, refs[9], refs[10], w, n, s),
+                        stream, "bsa_decode", tensors)
+    return out, lse, workspace

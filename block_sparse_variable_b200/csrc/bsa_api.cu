@@ -7,6 +7,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "args.h"
 #include "bsa_internal.h"
 
 namespace bsa {
@@ -28,7 +29,15 @@ int num_sms() {
 
 namespace {
 
+using bsa::at;
+using bsa::block_ok;
+using bsa::cdiv;
+using bsa::check_values;
+using bsa::place;
+using bsa::present;
 using bsa::Problem;
+using bsa::same_shape;
+using bsa::vec_ok;
 
 struct Args {
   const bsa_tensor *q, *k, *v, *index, *cu_q, *cu_kv, *seqused, *bt, *out, *lse;
@@ -37,52 +46,11 @@ struct Args {
   bool bwd;
 };
 
-bool present(const bsa_tensor *t) { return t != nullptr && t->data != nullptr; }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool block_ok(int64_t x) { return x == 128 || x == 256 || x == 512 || x == 1024; }
-
-// A dense-value tensor (q/k/v/out/...): given ndim, dtype, last stride 1, the
-// other strides 16-byte multiples (8 16-bit or 16 8-bit elements) and a
-// 16-byte-aligned base (16-byte vector loads and TMA boxes start on 16-byte
-// boundaries).
-bsa_status check_values(const bsa_tensor *t, int ndim, int dtype) {
-  if (t->ndim != ndim || t->dtype != dtype) return BSA_ERR_PARAM_INVALID;
-  if (t->stride[ndim - 1] != 1) return BSA_ERR_PARAM_INVALID;
-  const int64_t per16 = dtype == BSA_F8E4M3 ? 16 : 8;
-  for (int i = 0; i < ndim; ++i) {
-    if (t->shape[i] < 0) return BSA_ERR_PARAM_INVALID;
-    if (i < ndim - 1 && (t->stride[i] % per16 != 0 || t->stride[i] < 0)) return BSA_ERR_PARAM_INVALID;
-  }
-  if (reinterpret_cast<uintptr_t>(t->data) % 16 != 0) return BSA_ERR_PARAM_INVALID;
-  return BSA_OK;
-}
-
-bool same_shape(const bsa_tensor *a, const bsa_tensor *b) {
-  if (a->ndim != b->ndim || a->dtype != b->dtype) return false;
-  for (int i = 0; i < a->ndim; ++i)
-    if (a->shape[i] != b->shape[i]) return false;
-  return true;
-}
-
-bool vec_ok(const bsa_tensor *t, int dtype, int64_t n) {
-  return t->ndim == 1 && t->dtype == dtype && t->shape[0] == n && (n <= 1 || t->stride[0] == 1);
-}
-
 struct Layout {
   bsa_ws_layout pub;
   // private regions
   bsa_ws_region row_batch, kb_batch, sorted, inv_cnt, inv_sub;
 };
-
-uint64_t place(uint64_t &cur, uint64_t bytes, bsa_ws_region &r) {
-  cur = (cur + 255) & ~uint64_t(255);
-  r.offset = cur;
-  r.bytes = bytes;
-  cur += bytes;
-  return r.offset;
-}
 
 // Validates every descriptor and fills the problem sizes, tensor views and
 // workspace layout.  Returns BSA_OK with p.B == 0 ... for an empty problem.
@@ -314,11 +282,6 @@ bsa_status prepare(const Args &a, Problem &p, Layout &L, bool &empty) {
   W_.tk_max = tk_max;
   W_.total_bytes = (cur + 255) & ~uint64_t(255);
   return BSA_OK;
-}
-
-template <typename T>
-T *at(void *ws, const bsa_ws_region &r) {
-  return r.bytes ? reinterpret_cast<T *>(static_cast<char *>(ws) + r.offset) : nullptr;
 }
 
 void carve(Problem &p, const Layout &L, void *ws) {

@@ -1,0 +1,223 @@
+// decode_plan.cuh -- how the few-token attention is divided among the blocks
+// of its grid, and the walk over the kv tokens of a unit.
+//
+// A unit is one tile of query rows (the heads of a kv head's group and the
+// query tokens, token-major: they read the same keys) against the kv tokens
+// it sees, cut into chunks.  The chunks of all units form one line, ordered
+// by sequence, head, tile, and block c of G takes the c-th G-th of it: every
+// block has the same number of chunks (within one) whatever the lengths
+// are.  A unit that lies within one block is finished there; the parts of
+// one that does not go to the workspace and a second kernel joins them.  A
+// block starts at most one part at its beginning and one at its end, hence
+// two slots each.
+#pragma once
+
+#include <limits.h>
+
+#include "cache.h"
+
+namespace bsa {
+namespace {
+
+struct DecBatch {
+  QBatch q;
+  KvBatch kv;
+  int nk;       // kv blocks (sparse)
+  int tiles;    // row tiles per head
+  int chunks;   // chunks of a unit
+  int64_t work; // chunks of all units of the batch
+};
+
+__device__ __forceinline__ DecBatch dec_batch(const DecodeProblem &p, int b, uint32_t &flags) {
+  DecBatch d;
+  d.q = q_batch(p.cu_q, p.Sq, p.Tq, b, flags);
+  d.kv = kv_batch(p.kv, b, flags);
+  d.nk = (d.kv.kvlen + p.kv.BKV - 1) / p.kv.BKV;
+  const int64_t gg = p.gg;
+  int64_t tiles;
+  if (p.index) {  // a tile's rows share an index row: tiles do not cross query blocks
+    const int full = d.q.qlen / p.BQ, rem = d.q.qlen % p.BQ;
+    tiles = int64_t(full) * ((p.BQ * gg + p.TR - 1) / p.TR) + (rem * gg + p.TR - 1) / p.TR;
+    d.chunks = max(1, min(p.W, d.nk) * (p.kv.BKV / p.chunk));
+  } else {
+    tiles = (d.q.qlen * gg + p.TR - 1) / p.TR;
+    d.chunks = max(1, (d.kv.kvlen + p.chunk - 1) / p.chunk);
+  }
+  d.tiles = int(tiles);
+  d.work = tiles * p.H * d.chunks;
+  return d;
+}
+
+// where a block of the grid begins and how far it goes
+struct DecStart {
+  int64_t total, lo, hi;  // chunks of the call; this block's range
+  int64_t rem;            // first chunk within batch b
+  int64_t blocks;         // blocks that have work
+  int b, qoff;            // batch of the first chunk; index rows of the batches before it
+};
+
+// by the whole block of kThreads threads; flags: contradictory lengths
+template <int kThreads>
+__device__ DecStart dec_start(const DecodeProblem &p, uint32_t &flags) {
+  __shared__ int64_t s_work[kThreads / 32], s_rows[kThreads / 32];
+  __shared__ DecStart s_start;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int64_t work = 0, rows = 0;
+  for (int b = b0; b < b1; ++b) {
+    const DecBatch d = dec_batch(p, b, flags);
+    work += d.work;
+    rows += (d.q.qlen + p.BQ - 1) / p.BQ;
+  }
+  int64_t iw = work, ir = rows;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, iw, o), y = __shfl_up_sync(0xffffffffu, ir, o);
+    if (lane >= o) iw += x, ir += y;
+  }
+  if (lane == 31) s_work[warp] = iw, s_rows[warp] = ir;
+  __syncthreads();
+  int64_t total = 0, bw = iw - work, br = ir - rows;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) bw += s_work[w], br += s_rows[w];
+    total += s_work[w];
+  }
+  const int64_t G = gridDim.x < total ? int64_t(gridDim.x) : total;
+  const int64_t c = blockIdx.x;
+  const int64_t lo = c < G ? c * total / G : total, hi = c < G ? (c + 1) * total / G : total;
+  if (c < G) {
+    if (lo >= bw && lo < bw + work) {
+      uint32_t ignore = 0;
+      for (int b = b0; b < b1; ++b) {
+        const DecBatch d = dec_batch(p, b, ignore);
+        if (lo < bw + d.work) {
+          s_start = {total, lo, hi, lo - bw, G, b, int(br)};
+          break;
+        }
+        bw += d.work;
+        br += (d.q.qlen + p.BQ - 1) / p.BQ;
+      }
+    }
+  } else if (tid == 0) {
+    s_start = {total, total, total, 0, G, 0, 0};
+  }
+  __syncthreads();
+  return s_start;
+}
+
+// a block's share of one unit
+struct DecSeg {
+  int hh, tile, cs, ce;  // head group, row tile, chunks [cs, ce)
+};
+
+// the query rows of a tile
+struct DecRows {
+  int t0, first, rows;  // row r: token t0 + (first + r) / gg, head hh * gg + (first + r) % gg
+  int irow;             // query block within the batch (sparse)
+};
+__device__ __forceinline__ DecRows dec_rows(const DecodeProblem &p, const DecBatch &d, int tile) {
+  DecRows v;
+  if (p.index) {
+    const int tpb = int((int64_t(p.BQ) * p.gg + p.TR - 1) / p.TR);
+    v.irow = tile / tpb;
+    v.t0 = v.irow * p.BQ;
+    v.first = (tile % tpb) * p.TR;
+    v.rows = min(p.TR, min(p.BQ, d.q.qlen - v.t0) * p.gg - v.first);
+  } else {
+    v.irow = 0;
+    v.t0 = int(int64_t(tile) * p.TR / p.gg);
+    v.first = int(int64_t(tile) * p.TR % p.gg);
+    v.rows = int(min(int64_t(p.TR), int64_t(d.q.qlen) * p.gg - int64_t(tile) * p.TR));
+  }
+  return v;
+}
+
+// The chunks of a segment, 32 at a time, one a lane: lane i holds the first
+// token of chunk base + i (-1: nothing there) and its page.  Sparse: chunk x
+// is chunk x % cpb of the (x / cpb)-th accepted entry of the index row.
+struct DecWalk {
+  const uint16_t *row;  // index row, null when dense
+  int slot, last;       // next slot to look at, highest accepted entry so far
+  int taken;            // entries accepted so far
+  uint32_t flags;
+};
+
+__device__ __forceinline__ DecWalk walk_begin(const DecodeProblem &p, int b, int hh, int irow, int qoff) {
+  DecWalk w{nullptr, 0, -1, 0, 0};
+  if (p.index) {
+    // fewer index rows than the lengths need: such a row selects nothing
+    const bool have = p.cu_q ? qoff + irow < p.R : true;
+    if (!have) { w.slot = p.W; w.flags = BSA_FLAG_BAD_INDEX; }
+    w.row = p.cu_q ? p.index + int64_t(hh) * p.ix_s0 + (have ? int64_t(qoff + irow) * p.ix_s1 : 0)
+                   : p.index + int64_t(b) * p.ix_s0 + int64_t(hh) * p.ix_s1 + int64_t(irow) * p.ix_s2;
+  }
+  return w;
+}
+
+// accept entries up to number `until`, by a converged warp; entry number
+// first + i goes to blk[i] (shared memory of the warp)
+__device__ __forceinline__ void walk_accept(const DecodeProblem &p, int nk, DecWalk &w, int first, int until,
+                                            int *blk, int lane) {
+  while (w.taken < until && w.slot < p.W) {
+    const int s = w.slot + lane;
+    const int e = s < p.W ? int(w.row[s]) : int(kNoBlock);
+    const bool used = e != int(kNoBlock), in = used && e < nk;
+    int pre = in ? e : -1;  // inclusive maximum of the entries in range
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre = max(pre, x);
+    }
+    int before = __shfl_up_sync(0xffffffffu, pre, 1);
+    before = max(lane ? before : -1, w.last);
+    const bool take = in && e > before;
+    const uint32_t m = __ballot_sync(0xffffffffu, take);
+    const int room = until - w.taken, rank = __popc(m & ((1u << lane) - 1u));
+    // slots past the last entry that is wanted are looked at again next time
+    const bool keep = take && rank < room;
+    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+    const int n = __popc(kept);
+    const int end = n == room ? 32 - __clz(kept) : 32;  // slots consumed
+    if (keep && w.taken + rank >= first) blk[w.taken + rank - first] = e;
+    if (__any_sync(0xffffffffu, lane < end && used && !take)) w.flags |= BSA_FLAG_BAD_INDEX;
+    w.last = max(w.last, __shfl_sync(0xffffffffu, pre, end - 1));
+    w.taken += n;
+    w.slot += end;
+  }
+  __syncwarp();
+}
+
+// Chunks [x, x + 32) of the unit, one a lane; x is a multiple of 32, so that
+// no entry is divided between two fetches.  blk: 16 words of the warp.
+__device__ __forceinline__ void walk_fetch(const DecodeProblem &p, const DecBatch &d, int b, DecWalk &w, int x,
+                                           int ce, int *blk, int lane, int &u, int &page) {
+  u = -1;
+  page = 0;
+  if (p.index) {
+    const int cpb = p.kv.BKV / p.chunk;  // 1 .. 16
+    const int first = x / cpb;
+    // the unit's last fetch reads the rest of the row, for its bad entries
+    const int until = x + 32 >= d.chunks ? INT_MAX : (x + 32) / cpb;
+    walk_accept(p, d.nk, w, first, until, blk, lane);
+    const int e = (x + lane) / cpb;
+    if (x + lane < ce && e < w.taken) u = blk[e - first] * p.kv.BKV + (x + lane) % cpb * p.chunk;
+    __syncwarp();
+  } else if (x + lane < ce) {
+    u = (x + lane) * p.chunk;
+  }
+  if (u >= d.kv.kvlen) u = -1;
+  if (u >= 0) {
+    page = kv_page_of(p.kv, b, u);
+    if (page < 0) { u = -1; w.flags |= BSA_FLAG_BAD_PAGE; }
+  }
+}
+
+// the block that owns chunk x of `total` among `blocks`
+__device__ __forceinline__ int64_t dec_owner(int64_t x, int64_t total, int64_t blocks) {
+  return ((x + 1) * blocks - 1) / total;
+}
+
+}  // namespace
+}  // namespace bsa

@@ -252,6 +252,105 @@ bsa_status bsa_bwd(const bsa_tensor *q, const bsa_tensor *k, const bsa_tensor *v
                    const bsa_tensor *dq, const bsa_tensor *dk, const bsa_tensor *dv,
                    void *workspace, size_t workspace_bytes, void *stream);
 
+/* ----------------------------------------------------- cache operators */
+/* Serving over a kv cache and block selection: means of the keys of every kv
+ * block, a block index chosen by the scores of those means, and attention of
+ * a few query tokens per sequence over the whole cache or the chosen blocks.
+ * (Additions of this library; the layouts, descriptors, lengths, block table
+ * and status bits are those of the attention passes.)  16-bit q / k / v; D in
+ * {64, 128}; fewer than 2^30 tokens stored per sequence or packed tensor.
+ *
+ * bsa_block_means:
+ *     means[b,h,j,:] = (1/n_j) sum of k[b,u,h,:]
+ * over the n_j tokens u of kv block j (block_shape[1] tokens) with
+ * u < kvlen_b and a valid page (none: zeros), summed in fp32.
+ *   k, cu_seqlens_kv, seqused_kv, block_table   as for bsa_fwd (params gives
+ *             the layout, num_kv_heads and block_shape; num_heads counts only
+ *             where num_kv_heads is 0)
+ *   first_kv  I32 [B], optional: only the blocks j >= first_kv[b] /
+ *             block_shape[1] are written (tokens from first_kv[b] on were
+ *             appended); a negative entry counts as 0 (BAD_SEQLEN)
+ *   means     [B, N2, NB, D], dtype of k; NB <= 65535.  Blocks at or past
+ *             ceil(kvlen_b / block_shape[1]) are left as they were; a kvlen_b
+ *             past NB blocks raises BAD_SEQLEN and those blocks are left out.
+ * BAD_PAGE is raised for table entries that a written block covers. */
+bsa_status bsa_block_means_get_workspace(const bsa_tensor *k, const bsa_tensor *cu_seqlens_kv,
+                                         const bsa_tensor *seqused_kv,
+                                         const bsa_tensor *block_table,
+                                         const bsa_tensor *first_kv, const bsa_params *params,
+                                         const bsa_tensor *means, size_t *workspace_bytes);
+
+bsa_status bsa_block_means(const bsa_tensor *k, const bsa_tensor *cu_seqlens_kv,
+                           const bsa_tensor *seqused_kv, const bsa_tensor *block_table,
+                           const bsa_tensor *first_kv, const bsa_params *params,
+                           const bsa_tensor *means, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* bsa_select_blocks: the index of bsa_fwd, bsa_bwd and bsa_decode from
+ *     s(hi,i,j) = (sum of the rows of query block i over the q heads of hi) . means[b,h2,j]
+ * Each index row keeps the W blocks (W = the index's width) of the highest
+ * score, ties to the lower id, in ascending order, padded with 0xFFFF.  The
+ * first sink_blocks and the last local_blocks of the candidates rank above
+ * every score.  Candidates are the sequence's kv blocks; with the causal mask
+ * those that the last row of the query block sees (a query block that sees
+ * none gets an empty row).  Scores are 64-bit; a NaN ranks below every number.
+ *   q, cu_seqlens_q             as for bsa_fwd (block_shape[0] rows a block)
+ *   means                       [B, N2, NB, D] of bsa_block_means, dtype of q
+ *   cu_seqlens_kv, seqused_kv   the kv lengths as for bsa_fwd (BNSD without
+ *             seqused_kv: NB * block_shape[1]); a length past NB blocks raises
+ *             BAD_SEQLEN and the blocks past NB are no candidates
+ *   index     U16, written: shape as for bsa_fwd, heads N1 or N2 (a row per q
+ *             head, or one per group).  Rows that belong to no query block are
+ *             left as they were; fewer rows than the lengths need raise
+ *             BAD_INDEX.
+ * The choice is piecewise constant in q and k, so it has no gradient: bsa_fwd
+ * and bsa_bwd with the index are the training pass. */
+bsa_status bsa_select_blocks_get_workspace(const bsa_tensor *q, const bsa_tensor *means,
+                                           const bsa_tensor *cu_seqlens_q,
+                                           const bsa_tensor *cu_seqlens_kv,
+                                           const bsa_tensor *seqused_kv, const bsa_params *params,
+                                           int64_t sink_blocks, int64_t local_blocks,
+                                           const bsa_tensor *index, size_t *workspace_bytes);
+
+bsa_status bsa_select_blocks(const bsa_tensor *q, const bsa_tensor *means,
+                             const bsa_tensor *cu_seqlens_q, const bsa_tensor *cu_seqlens_kv,
+                             const bsa_tensor *seqused_kv, const bsa_params *params,
+                             int64_t sink_blocks, int64_t local_blocks, const bsa_tensor *index,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* bsa_decode: out = softmax(scale Q K^T + mask) V and its lse for a few query
+ * tokens per sequence (any number is right; bsa_fwd is the pass for prompts).
+ * Forward only.
+ *   q, k, v, cu_seqlens_*, seqused_kv, block_table, out, lse   as for bsa_fwd
+ *   index      optional (absent: the whole cache): as for bsa_fwd, one row per
+ *              query block of block_shape[0] tokens
+ *   tree_mask  optional, I64, with mask_type BSA_MASK_NONE: the query tokens
+ *              of a sequence are the nodes of a draft tree, and the last qlen
+ *              tokens of its cache are their keys.  [Tq, words] (TND) or
+ *              [B, Sq, words] (BNSD, words >= ceil(Sq / 64)): query t sees node
+ *              j iff bit j % 64 of word j / 64 of its row is set (its ancestors
+ *              and itself), and every token before the drafts.  Nodes past the
+ *              words are not seen.
+ * mask_type BSA_MASK_CAUSAL is the chain: node j is seen iff j <= t.  A row
+ * that sees nothing gets out 0, lse -inf; rows of no sequence are left as they
+ * were.  Bitwise the same on every run.  Weights are rounded to the inputs'
+ * type before their product with V; sums are fp32.  BAD_INDEX as for bsa_fwd;
+ * BAD_PAGE is raised for table entries whose tokens a row selects. */
+bsa_status bsa_decode_get_workspace(const bsa_tensor *q, const bsa_tensor *k, const bsa_tensor *v,
+                                    const bsa_tensor *index, const bsa_tensor *tree_mask,
+                                    const bsa_tensor *cu_seqlens_q,
+                                    const bsa_tensor *cu_seqlens_kv, const bsa_tensor *seqused_kv,
+                                    const bsa_tensor *block_table, const bsa_params *params,
+                                    const bsa_tensor *out, const bsa_tensor *lse,
+                                    size_t *workspace_bytes);
+
+bsa_status bsa_decode(const bsa_tensor *q, const bsa_tensor *k, const bsa_tensor *v,
+                      const bsa_tensor *index, const bsa_tensor *tree_mask,
+                      const bsa_tensor *cu_seqlens_q, const bsa_tensor *cu_seqlens_kv,
+                      const bsa_tensor *seqused_kv, const bsa_tensor *block_table,
+                      const bsa_params *params, const bsa_tensor *out, const bsa_tensor *lse,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
 /* ----------------------------------------------------- status, layout */
 /* Synchronises `stream`, then copies the workspace's status word (the
  * BSA_FLAG_* bits raised by the last call that used this workspace). */
