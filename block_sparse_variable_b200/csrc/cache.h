@@ -86,6 +86,8 @@ struct DecodeProblem {
 cudaError_t launch_block_means(const MeansProblem &p, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectProblem &p, cudaStream_t s);
 cudaError_t launch_decode(const DecodeProblem &p, cudaStream_t s);
+cudaError_t launch_decode_tc(const DecodeProblem &p, cudaStream_t s);
+void decode_tc_plan(DecodeProblem &p);
 // fills the tile, step and grid of a problem whose sizes are set
 void decode_plan(DecodeProblem &p);
 

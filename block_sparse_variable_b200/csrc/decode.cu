@@ -24,6 +24,9 @@ constexpr int kThreads = 128, kWarps = 4;
 constexpr int kChunk = 64;   // tokens of a step, 16 a warp
 constexpr int kTile = 16;    // query rows of a tile
 constexpr int kStages = 3;
+// query rows of a kv head's group up to which this kernel is taken; above,
+// the tensor core kernel with 128-row tiles
+constexpr int kFewRows = 16;
 
 template <int D>
 struct Smem {
@@ -32,8 +35,8 @@ struct Smem {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kRing = kStages * kStage;          // of one warp
   static constexpr int kMl = kWarps * kRing;              // [warps][rows][2] floats
-  static constexpr int kBlk = kMl + kWarps * kTile * 8;   // [warps][16] ints
-  static constexpr int kU = kBlk + kWarps * 64;           // [warps][stages] first token of a stage
+  static constexpr int kBlk = kMl + kWarps * kTile * 8;   // [warps][32] ints
+  static constexpr int kU = kBlk + kWarps * 128;          // [warps][stages] first token of a stage
   static constexpr int kBytes = kU + kWarps * kStages * 4;
   static_assert(kWarps * kTile * D * 4 <= kWarps * kRing, "the states are joined in the ring's memory");
 };
@@ -71,23 +74,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T>
-__device__ __forceinline__ void write_row(const DecodeProblem &p, const DecBatch &d, const DecRows &v, int b,
-                                          int hh, int r, int D4, float4 o, float m, float l) {
-  // columns [4 D4, 4 D4 + 4) of tile row r; o unnormalised, m in log2 units
-  const int x = v.first + r, t = v.t0 + x / p.gg, h = hh * p.gg + x % p.gg;
-  const int64_t qb = p.cu_q ? 0 : b;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  uint2 w;
-  w.x = Pack2<T>::pack(o.x * inv, o.y * inv);
-  w.y = Pack2<T>::pack(o.z * inv, o.w * inv);
-  T *dst = static_cast<T *>(p.out) + qb * p.o_sb + (d.q.tok0 + t) * p.o_st + int64_t(h) * p.o_sh;
-  reinterpret_cast<uint2 *>(dst)[D4] = w;
-  if (D4 == 0 && p.lse)
-    p.lse[qb * p.l_sb + (d.q.tok0 + t) * p.l_st + int64_t(h) * p.l_sh] =
-        l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-}
-
 // mask of one (row, kv token) pair of the last qlen tokens
 template <int kMask>  // 0 none, 1 causal, 2 tree
 __device__ __forceinline__ bool seen(const DecodeProblem &p, const int64_t *bits, int t, int node) {
@@ -110,35 +96,26 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
   griddep_wait();
   griddep_launch_next();
   uint32_t flags = 0;
-  const DecStart st = dec_start<kThreads>(p, flags);
+  __shared__ DecScratch<kThreads> scratch;
+  const DecStart st = dec_start<kThreads>(p, scratch, flags);
   const uint32_t ring = smem_u32(smem) + uint32_t(warp * S::kRing);
   float *s_o = reinterpret_cast<float *>(smem);
   float2 *s_ml = reinterpret_cast<float2 *>(smem + S::kMl);
-  int *s_blk = reinterpret_cast<int *>(smem + S::kBlk) + warp * 16;  // 32 chunks of 64 are 16 blocks at most
+  int *s_blk = reinterpret_cast<int *>(smem + S::kBlk) + warp * 32;
   int *s_u = reinterpret_cast<int *>(smem + S::kU) + warp * kStages;
   DecodeJoin join{0, 0, 0, 0, 0};
 
-  int64_t pos = st.lo, rem = st.rem;
-  int b = st.b, qoff = st.qoff;
-  while (pos < st.hi) {
-    uint32_t ignore = 0;
-    const DecBatch d = dec_batch(p, b, ignore);
-    if (rem >= d.work) {
-      rem -= d.work;
-      qoff += (d.q.qlen + p.BQ - 1) / p.BQ;
-      ++b;
-      continue;
-    }
-    const int64_t unit = rem / d.chunks;
-    const int cs = int(rem % d.chunks);
-    const int ce = int(min(int64_t(d.chunks), cs + (st.hi - pos)));
-    const int hh = int(unit / d.tiles), tile = int(unit % d.tiles);
+  DecCursor cursor = cursor_begin(st), here;
+  DecBatch d;
+  DecSeg seg;
+  while (cursor_next(p, st, cursor, d, seg, here)) {
+    const int b = here.b, hh = seg.hh, tile = seg.tile, cs = seg.cs, ce = seg.ce;
     const int h2 = hh / (p.H / p.N2);
     const DecRows v = dec_rows(p, d, tile);
     const int qbase = d.kv.kvlen - d.q.qlen;  // kv token of draft node 0
 
     // ---- the first stages, then Q while they fly
-    DecWalk w = walk_begin(p, b, hh, v.irow, qoff);
+    DecWalk w = walk_begin(p, b, hh, v.irow, here.qoff);
     int cu, cpg, nu = -1, npg = 0;
     walk_fetch(p, d, b, w, cs & ~31, ce, s_blk, lane, cu, cpg);
     const int sub = lane / kLanes, col = lane % kLanes;
@@ -149,14 +126,14 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
         const int s = x % kStages;
         if (lane == 0) s_u[s] = u0;
         if (u0 >= 0) {
-          const int u = u0 + 16 * warp, here = d.kv.kvlen - u;
+          const int u = u0 + 16 * warp, left = d.kv.kvlen - u;
           const T *k = static_cast<const T *>(p.k) + kv_off(p.kv, p.k_sb, p.k_sh, p.k_st, d.kv, b, h2, u, pg);
           const T *vv = static_cast<const T *>(p.v) + kv_off(p.kv, p.v_sb, p.v_sh, p.v_st, d.kv, b, h2, u, pg);
           const uint32_t at = ring + uint32_t(s * S::kStage);
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             const int r = sub + i * (32 / kLanes);
-            const bool in = r < here;
+            const bool in = r < left;
             const uint32_t dst = at + uint32_t(r * S::kRow + ((col ^ (r & 7)) << 4));
             cp_async16(dst, in ? k + int64_t(r) * p.k_st + col * 8 : static_cast<const T *>(p.k), in);
             cp_async16(dst + S::kHalf, in ? vv + int64_t(r) * p.v_st + col * 8 : static_cast<const T *>(p.v), in);
@@ -291,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
     }
     __syncthreads();
     const bool whole = cs == 0 && ce == d.chunks;
-    const int slot = pos == st.lo ? 2 * int(blockIdx.x) : 2 * int(blockIdx.x) + 1;
+    const int slot = here.pos == st.lo ? 2 * int(blockIdx.x) : 2 * int(blockIdx.x) + 1;
     for (int i = tid; i < v.rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), c = i % (D / 4);
       float mm = -INFINITY, ll = 0.f;
@@ -319,9 +296,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
     }
     __syncthreads();
     if (cs == 0 && !whole)
-      join = {b, hh, tile, int(dec_owner(pos + d.chunks - 1, st.total, st.blocks) - blockIdx.x) + 1, slot};
-    pos += ce - cs;
-    rem += ce - cs;
+      join = {b, hh, tile, int(dec_owner(here.pos + d.chunks - 1, st.total, st.blocks) - blockIdx.x) + 1, slot};
   }
   __shared__ uint32_t s_flags;
   if (tid == 0) s_flags = 0;
@@ -394,6 +369,12 @@ __global__ void __launch_bounds__(kThreads) k_decode_join(const DecodeProblem p)
   }
 }
 
+template <int D, typename T>
+cudaError_t launch_join(const DecodeProblem &p, cudaStream_t s) {
+  return launch_dep(k_decode_join<D, T>, dim3(unsigned(p.grid), unsigned((p.TR + kWarps - 1) / kWarps)),
+                    dim3(kThreads), 0, s, p);
+}
+
 template <int D, typename T, int kMask>
 cudaError_t launch(const DecodeProblem &p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_decode<D, T, kMask>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -401,8 +382,7 @@ cudaError_t launch(const DecodeProblem &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_dep(k_decode<D, T, kMask>, dim3(unsigned(p.grid)), dim3(kThreads), Smem<D>::kBytes, s, p);
   if (e != cudaSuccess) return e;
-  return launch_dep(k_decode_join<D, T>, dim3(unsigned(p.grid), unsigned((p.TR + kWarps - 1) / kWarps)),
-                    dim3(kThreads), 0, s, p);
+  return launch_join<D, T>(p, s);
 }
 
 template <int D, typename T>
@@ -414,12 +394,21 @@ cudaError_t launch_mask(const DecodeProblem &p, cudaStream_t s) {
 }  // namespace
 
 void decode_plan(DecodeProblem &p) {
+  const int64_t tokens = p.q_layout == BSA_LAYOUT_BNSD ? p.Sq : (p.Tq + p.B - 1) / p.B;
+  if (tokens * p.gg > kFewRows) return decode_tc_plan(p);
   p.TR = kTile;
   p.chunk = kChunk;
   p.grid = num_sms() * (p.D == 128 ? 2 : 4);
 }
 
 cudaError_t launch_decode(const DecodeProblem &p, cudaStream_t s) {
+  if (p.TR != kTile) {
+    cudaError_t e = launch_decode_tc(p, s);
+    if (e != cudaSuccess) return e;
+    if (p.dtype == BSA_BF16)
+      return p.D == 64 ? launch_join<64, __nv_bfloat16>(p, s) : launch_join<128, __nv_bfloat16>(p, s);
+    return p.D == 64 ? launch_join<64, __half>(p, s) : launch_join<128, __half>(p, s);
+  }
   if (p.dtype == BSA_BF16)
     return p.D == 64 ? launch_mask<64, __nv_bfloat16>(p, s) : launch_mask<128, __nv_bfloat16>(p, s);
   return p.D == 64 ? launch_mask<64, __half>(p, s) : launch_mask<128, __half>(p, s);

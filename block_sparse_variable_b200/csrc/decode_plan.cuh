@@ -15,6 +15,7 @@
 #include <limits.h>
 
 #include "cache.h"
+#include "pack16.cuh"
 
 namespace bsa {
 namespace {
@@ -56,11 +57,15 @@ struct DecStart {
   int b, qoff;            // batch of the first chunk; index rows of the batches before it
 };
 
+template <int kThreads>
+struct DecScratch {
+  int64_t work[kThreads / 32], rows[kThreads / 32];
+  DecStart start;
+};
+
 // by the whole block of kThreads threads; flags: contradictory lengths
 template <int kThreads>
-__device__ DecStart dec_start(const DecodeProblem &p, uint32_t &flags) {
-  __shared__ int64_t s_work[kThreads / 32], s_rows[kThreads / 32];
-  __shared__ DecStart s_start;
+__device__ DecStart dec_start(const DecodeProblem &p, DecScratch<kThreads> &sh, uint32_t &flags) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -76,24 +81,24 @@ __device__ DecStart dec_start(const DecodeProblem &p, uint32_t &flags) {
     const int64_t x = __shfl_up_sync(0xffffffffu, iw, o), y = __shfl_up_sync(0xffffffffu, ir, o);
     if (lane >= o) iw += x, ir += y;
   }
-  if (lane == 31) s_work[warp] = iw, s_rows[warp] = ir;
+  if (lane == 31) sh.work[warp] = iw, sh.rows[warp] = ir;
   __syncthreads();
   int64_t total = 0, bw = iw - work, br = ir - rows;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) bw += s_work[w], br += s_rows[w];
-    total += s_work[w];
+    if (w < warp) bw += sh.work[w], br += sh.rows[w];
+    total += sh.work[w];
   }
   const int64_t G = gridDim.x < total ? int64_t(gridDim.x) : total;
   const int64_t c = blockIdx.x;
-  const int64_t lo = c < G ? c * total / G : total, hi = c < G ? (c + 1) * total / G : total;
   if (c < G) {
+    const int64_t lo = c * total / G;
     if (lo >= bw && lo < bw + work) {
       uint32_t ignore = 0;
       for (int b = b0; b < b1; ++b) {
         const DecBatch d = dec_batch(p, b, ignore);
         if (lo < bw + d.work) {
-          s_start = {total, lo, hi, lo - bw, G, b, int(br)};
+          sh.start = {total, lo, (c + 1) * total / G, lo - bw, G, b, int(br)};
           break;
         }
         bw += d.work;
@@ -101,10 +106,10 @@ __device__ DecStart dec_start(const DecodeProblem &p, uint32_t &flags) {
       }
     }
   } else if (tid == 0) {
-    s_start = {total, total, total, 0, G, 0, 0};
+    sh.start = {total, total, total, 0, G, 0, 0};
   }
   __syncthreads();
-  return s_start;
+  return sh.start;
 }
 
 // a block's share of one unit
@@ -190,7 +195,7 @@ __device__ __forceinline__ void walk_accept(const DecodeProblem &p, int nk, DecW
 }
 
 // Chunks [x, x + 32) of the unit, one a lane; x is a multiple of 32, so that
-// no entry is divided between two fetches.  blk: 16 words of the warp.
+// no entry is divided between two fetches.  blk: 32 words of the warp.
 __device__ __forceinline__ void walk_fetch(const DecodeProblem &p, const DecBatch &d, int b, DecWalk &w, int x,
                                            int ce, int *blk, int lane, int &u, int &page) {
   u = -1;
@@ -212,6 +217,54 @@ __device__ __forceinline__ void walk_fetch(const DecodeProblem &p, const DecBatc
     page = kv_page_of(p.kv, b, u);
     if (page < 0) { u = -1; w.flags |= BSA_FLAG_BAD_PAGE; }
   }
+}
+
+// A block's place on the line: the segment it is at.
+struct DecCursor {
+  int64_t pos, rem;  // chunk of the line, chunk within the batch
+  int b, qoff;
+};
+__device__ __forceinline__ DecCursor cursor_begin(const DecStart &s) { return {s.lo, s.rem, s.b, s.qoff}; }
+// the segment at the cursor, which is then moved past it; false at the end
+__device__ __forceinline__ bool cursor_next(const DecodeProblem &p, const DecStart &s, DecCursor &c, DecBatch &d,
+                                            DecSeg &g, DecCursor &at) {
+  while (c.pos < s.hi) {
+    uint32_t ignore = 0;
+    d = dec_batch(p, c.b, ignore);
+    if (c.rem >= d.work) {
+      c.rem -= d.work;
+      c.qoff += (d.q.qlen + p.BQ - 1) / p.BQ;
+      ++c.b;
+      continue;
+    }
+    const int64_t unit = c.rem / d.chunks;
+    g.cs = int(c.rem % d.chunks);
+    g.ce = int(min(int64_t(d.chunks), g.cs + (s.hi - c.pos)));
+    g.hh = int(unit / d.tiles);
+    g.tile = int(unit % d.tiles);
+    at = c;
+    c.pos += g.ce - g.cs;
+    c.rem += g.ce - g.cs;
+    return true;
+  }
+  return false;
+}
+
+template <typename T>
+__device__ __forceinline__ void write_row(const DecodeProblem &p, const DecBatch &d, const DecRows &v, int b,
+                                          int hh, int r, int D4, float4 o, float m, float l) {
+  // columns [4 D4, 4 D4 + 4) of tile row r; o unnormalised, m in log2 units
+  const int x = v.first + r, t = v.t0 + x / p.gg, h = hh * p.gg + x % p.gg;
+  const int64_t qb = p.cu_q ? 0 : b;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  uint2 w;
+  w.x = Pack2<T>::pack(o.x * inv, o.y * inv);
+  w.y = Pack2<T>::pack(o.z * inv, o.w * inv);
+  T *dst = static_cast<T *>(p.out) + qb * p.o_sb + (d.q.tok0 + t) * p.o_st + int64_t(h) * p.o_sh;
+  reinterpret_cast<uint2 *>(dst)[D4] = w;
+  if (D4 == 0 && p.lse)
+    p.lse[qb * p.l_sb + (d.q.tok0 + t) * p.l_st + int64_t(h) * p.l_sh] =
+        l > 0.f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // the block that owns chunk x of `total` among `blocks`

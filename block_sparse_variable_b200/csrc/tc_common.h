@@ -20,6 +20,9 @@ struct FwdMaps {
 
 cudaError_t make_fwd_maps(const Problem &p, FwdMaps &m);
 
+// the k and v maps alone (reads p's kv layout, sizes, strides, D and dtype)
+cudaError_t make_kv_maps(const Problem &p, CUtensorMap &k, CUtensorMap &v);
+
 // the backward also streams dOut with the q-tensor box, and adds its dQ
 // tiles into the fp32 accumulator [rows][N1][D] through a 3-D map
 // {D, N1, rows} with 32-column x 1-head x 128-row boxes (128-byte swizzle)

@@ -119,6 +119,11 @@ cudaError_t q_map_packed(CUtensorMap *m, const Problem &p) {
 
 }  // namespace
 
+cudaError_t make_kv_maps(const Problem &p, CUtensorMap &k, CUtensorMap &v) {
+  cudaError_t e = kv_map(&k, p, p.k, p.k_sb, p.k_sh, p.k_st);
+  return e != cudaSuccess ? e : kv_map(&v, p, p.v, p.v_sb, p.v_sh, p.v_st);
+}
+
 cudaError_t make_fwd_maps(const Problem &p, FwdMaps &m) {
   cudaError_t e = p.pack_g > 1 ? q_map_packed(&m.q, p) : q_map(&m.q, p, p.q, p.q_sb, p.q_sh, p.q_st);
   if (e != cudaSuccess) return e;
