@@ -4,12 +4,8 @@
 // that exist (u < kvlen_b, valid page).  One pass over the keys: memory
 // bound, one addition per element read, summed in fp32 and rounded once.
 //
-// One 256-thread block per (sequence, kv head, kv block): 16 bytes a thread,
-// D / 8 threads a row, the rows of a 128-row chunk (one page at most) all
-// requested before the first is used.  From first_kv on (an append touches
-// the last block or two of each sequence) a sequence gets a few blocks of
-// threads that stride over its kv blocks instead of one for every kv block
-// it could have.
+// One or eight warps per (sequence, kv head, kv block): 16 bytes a thread, D / 8
+// threads a row, up to 16 loads of a thread requested before the first is used.
 #include <cuda_runtime.h>
 
 #include "cache.h"
@@ -34,13 +30,22 @@ __device__ void check_inputs(const MeansProblem &p) {
     if (kb.kvlen > int64_t(p.NB) * p.kv.BKV) f |= BSA_FLAG_BAD_SEQLEN;
   }
   if (p.kv.table) {
-    for (int b = 0; b < p.kv.B; ++b) {
-      uint32_t g = 0;
-      const KvBatch kb = kv_batch(p.kv, b, g);
-      const int first = p.first_kv ? max(p.first_kv[b], 0) / p.kv.BKV * p.kv.BKV : 0;
-      for (int64_t u = int64_t(first) / p.kv.page_size + threadIdx.x; u * p.kv.page_size < kb.kvlen; u += kThreads) {
-        const int pg = p.kv.table[int64_t(b) * p.kv.bt_s0 + u];
-        if (pg < 0 || pg >= p.kv.num_pages) f |= BSA_FLAG_BAD_PAGE;
+    // a thread takes kRun consecutive entries of a sequence, so that the loads
+    // of many sequences are in flight together
+    constexpr int kRun = 16;
+    const int runs = (p.kv.max_pages + kRun - 1) / kRun;
+    for (int64_t id = threadIdx.x; id < int64_t(p.kv.B) * runs; id += kThreads) {
+      const int b = int(id / runs), run = int(id % runs);
+      uint32_t ignore = 0;
+      const KvBatch kb = kv_batch(p.kv, b, ignore);
+      const int used = (kb.kvlen + p.kv.page_size - 1) / p.kv.page_size;
+      const int first = p.first_kv ? max(p.first_kv[b], 0) / p.kv.BKV * p.kv.BKV / p.kv.page_size : 0;
+      const int x0 = first + run * kRun, n = min(kRun, used - x0);
+      const int32_t *row = p.kv.table + int64_t(b) * p.kv.bt_s0 + x0;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int pg = i < n ? row[i] : 0;
+        if (i < n && (pg < 0 || pg >= p.kv.num_pages)) f |= BSA_FLAG_BAD_PAGE;
       }
     }
   }
@@ -49,17 +54,31 @@ __device__ void check_inputs(const MeansProblem &p) {
   if (threadIdx.x < kStWords) p.status[threadIdx.x] = threadIdx.x == kStFlags ? sflags : 0;
 }
 
-template <int D, typename T>
+// volatile: the loads of a batch are issued before the first is used
+__device__ __forceinline__ uint4 load16(const void *p) {
+  uint4 x;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(p));
+  return x;
+}
+
+// kWarps warps share the rows of one kv block of one head
+template <int D, typename T, int kWarps>
 __global__ void __launch_bounds__(kThreads) k_block_means(const MeansProblem p, int slots) {
-  constexpr int kLanes = D / 8;                  // threads of a row, 16 bytes each
-  constexpr int kRows = kThreads / kLanes;       // rows in flight per load
-  constexpr int kLoads = 128 / kRows;            // loads of a 128-row chunk
+  constexpr int kLanes = D / 8;                       // threads of a row, 16 bytes each
+  constexpr int kRows = kWarps * 32 / kLanes;         // rows of one load
+  constexpr int kAll = 128 / kRows;                   // loads of a 128-row chunk
+  constexpr int kLoads = kAll < 16 ? kAll : 16;       // in flight together
   __shared__ float red[kThreads / 32][D];
   griddep_wait();
   griddep_launch_next();
   if (blockIdx.x == 0) return check_inputs(p);
-  int64_t id = int64_t(blockIdx.x) - 1;
-  // heads fastest: blocks that run together read neighbouring rows
+  const int tid = threadIdx.x % (32 * kWarps), lane = tid & 31, warp = tid >> 5;
+  const int64_t all = int64_t(p.kv.B) * slots * p.kv.N2;
+  int64_t id = (int64_t(blockIdx.x) - 1) * (kThreads / 32 / kWarps) + threadIdx.x / (32 * kWarps);
+  if (id >= all) return;  // whole warps; with kWarps == 8 whole blocks
+  // heads fastest: warps that run together read neighbouring rows
   const int h = int(id % p.kv.N2);
   id /= p.kv.N2;
   const int slot = int(id % slots), b = int(id / slots);
@@ -68,7 +87,6 @@ __global__ void __launch_bounds__(kThreads) k_block_means(const MeansProblem p, 
   const int BKV = p.kv.BKV;
   const int j0 = p.first_kv ? max(p.first_kv[b], 0) / BKV : 0;
   const int nk = min((kb.kvlen + BKV - 1) / BKV, p.NB);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int col = tid % kLanes, row = tid / kLanes;
   const T *k = static_cast<const T *>(p.k);
   for (int j = j0 + slot; j < nk; j += slots) {
@@ -83,20 +101,28 @@ __global__ void __launch_bounds__(kThreads) k_block_means(const MeansProblem p, 
       const int here = min(u_end - u0, 128);
       n += here;
       const T *src = k + kv_off(p.kv, p.k_sb, p.k_sh, p.k_st, kb, b, h, u0, pg) + col * 8;
-      uint4 x[kLoads];
+#pragma unroll 1
+      for (int i0 = 0; i0 < kAll; i0 += kLoads) {
+        if (i0 * kRows >= here) break;
+        uint4 x[kLoads];
+        const T *at = src + int64_t(row + i0 * kRows) * p.k_st;
+        if (here == 128) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int r = row + i * kRows;
-        x[i] = r < here ? __ldg(reinterpret_cast<const uint4 *>(src + int64_t(r) * p.k_st)) : make_uint4(0, 0, 0, 0);
-      }
+          for (int i = 0; i < kLoads; ++i) x[i] = load16(at + int64_t(i * kRows) * p.k_st);
+        } else {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          for (int i = 0; i < kLoads; ++i)
+            x[i] = row + (i0 + i) * kRows < here ? load16(at + int64_t(i * kRows) * p.k_st) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 f = Pack2<T>::unpack(w[c]);
-          acc[2 * c] += f.x;
-          acc[2 * c + 1] += f.y;
+        for (int i = 0; i < kLoads; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 f = Pack2<T>::unpack(w[c]);
+            acc[2 * c] += f.x;
+            acc[2 * c + 1] += f.y;
+          }
         }
       }
     }
@@ -104,36 +130,49 @@ __global__ void __launch_bounds__(kThreads) k_block_means(const MeansProblem p, 
     for (int o = kLanes; o < 32; o <<= 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    if (lane < kLanes)
+    const float d = n > 0 ? float(n) : 1.f;  // every page bad: zeros
+    T *dst = static_cast<T *>(p.means) + int64_t(b) * p.m_sb + int64_t(h) * p.m_sh + int64_t(j) * p.m_st;
+    if constexpr (kWarps == 1) {
+      if (lane < kLanes)
+        reinterpret_cast<uint4 *>(dst)[col] =
+            make_uint4(Pack2<T>::pack(acc[0] / d, acc[1] / d), Pack2<T>::pack(acc[2] / d, acc[3] / d),
+                       Pack2<T>::pack(acc[4] / d, acc[5] / d), Pack2<T>::pack(acc[6] / d, acc[7] / d));
+    } else {
+      if (lane < kLanes)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) red[warp][col * 8 + i] = acc[i];
-    __syncthreads();
-    if (tid < D / 2) {
-      float a = 0.f, c = 0.f;
+        for (int i = 0; i < 8; ++i) red[warp][col * 8 + i] = acc[i];
+      __syncthreads();
+      if (tid < D / 2) {
+        float a = 0.f, c = 0.f;
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        a += red[w][2 * tid];
-        c += red[w][2 * tid + 1];
+        for (int w = 0; w < kWarps; ++w) {
+          a += red[w][2 * tid];
+          c += red[w][2 * tid + 1];
+        }
+        reinterpret_cast<uint32_t *>(dst)[tid] = Pack2<T>::pack(a / d, c / d);
       }
-      const float d = n > 0 ? float(n) : 1.f;  // every page bad: zeros
-      T *dst = static_cast<T *>(p.means) + int64_t(b) * p.m_sb + int64_t(h) * p.m_sh + int64_t(j) * p.m_st;
-      reinterpret_cast<uint32_t *>(dst)[tid] = Pack2<T>::pack(a / d, c / d);
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
 template <int D, typename T>
 cudaError_t launch(const MeansProblem &p, cudaStream_t s) {
-  // a whole pass gives every kv block its own thread block; from first_kv on
-  // about eight thread blocks per SM walk the kv blocks there are
+  const int64_t pairs = int64_t(p.kv.B) * p.kv.N2, wide = int64_t(num_sms()) * 8;
+  // A whole pass gives every kv block a warp (no barrier, 8 KB of loads in
+  // flight a warp) once there are warps for the whole device; fewer blocks
+  // than that, and an append's, get eight warps each, for their latency.  An
+  // append's thread blocks stride over the kv blocks that there are.
+  if (!p.first_kv && pairs * p.NB >= 4 * wide) {
+    const int64_t grid = 1 + (pairs * p.NB + kThreads / 32 - 1) / (kThreads / 32);
+    return launch_dep(k_block_means<D, T, 1>, dim3(unsigned(grid)), dim3(kThreads), 0, s, p, int(p.NB));
+  }
   int64_t slots = p.NB;
   if (p.first_kv) {
-    const int64_t want = (int64_t(num_sms()) * 8 + int64_t(p.kv.B) * p.kv.N2 - 1) / (int64_t(p.kv.B) * p.kv.N2);
+    const int64_t want = (wide + pairs - 1) / pairs;
     slots = want < p.NB ? want : p.NB;
   }
-  const int64_t grid = 1 + int64_t(p.kv.B) * p.kv.N2 * slots;
-  return launch_dep(k_block_means<D, T>, dim3(unsigned(grid)), dim3(kThreads), 0, s, p, int(slots));
+  return launch_dep(k_block_means<D, T, 8>, dim3(unsigned(1 + pairs * slots)), dim3(kThreads), 0, s, p, int(slots));
 }
 
 }  // namespace

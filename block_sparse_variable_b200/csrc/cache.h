@@ -50,9 +50,12 @@ struct SelectProblem {
   uint64_t *keys;      // [Hidx][Rg][NB] order-preserving bits of the scores
 };
 
-// one split unit that a decode block begins: what the join kernel reads
+// a unit that a decode block begins and others finish: what the join kernel reads
 struct DecodeJoin {
-  int32_t b, hh, tile, parts, slot0;  // parts == 0: nothing to join
+  int64_t tok0;          // first query row of the sequence
+  int32_t b, hh;         // BNSD sequence (0 when packed), head group
+  int32_t t0, first, rows;  // the tile's rows (decode_plan.cuh: DecRows)
+  int32_t parts, slot0;  // parts == 0: nothing to join
 };
 
 struct DecodeProblem {
@@ -61,6 +64,7 @@ struct DecodeProblem {
   int32_t TR;         // query rows of a tile
   int32_t chunk;      // kv tokens of a work unit's step
   int32_t grid;       // blocks of the attention kernel
+  int32_t group;      // blocks that take the same chunks for different row tiles
   int32_t tree_words;
   int64_t Sq, Tq;
   float scale_log2;

@@ -74,6 +74,24 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// columns [4 c, 4 c + 4) of one output row, and its lse: row x of the head
+// group's rows from token t0 on; o unnormalised, m in log2 units
+template <typename T>
+__device__ __forceinline__ void write_row(const DecodeProblem &p, int64_t tok0, int b, int hh, int t0, int x, int c,
+                                          float4 o, float m, float l) {
+  const int t = t0 + x / p.gg, h = hh * p.gg + x % p.gg;
+  const bool some = l > 0.f || l != l;
+  const float inv = some ? 1.f / l : 0.f;
+  uint2 w;
+  w.x = Pack2<T>::pack(o.x * inv, o.y * inv);
+  w.y = Pack2<T>::pack(o.z * inv, o.w * inv);
+  T *dst = static_cast<T *>(p.out) + b * p.o_sb + (tok0 + t) * p.o_st + int64_t(h) * p.o_sh;
+  reinterpret_cast<uint2 *>(dst)[c] = w;
+  if (c == 0 && p.lse)
+    p.lse[b * p.l_sb + (tok0 + t) * p.l_st + int64_t(h) * p.l_sh] =
+        some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
 // mask of one (row, kv token) pair of the last qlen tokens
 template <int kMask>  // 0 none, 1 causal, 2 tree
 __device__ __forceinline__ bool seen(const DecodeProblem &p, const int64_t *bits, int t, int node) {
@@ -103,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
   float2 *s_ml = reinterpret_cast<float2 *>(smem + S::kMl);
   int *s_blk = reinterpret_cast<int *>(smem + S::kBlk) + warp * 32;
   int *s_u = reinterpret_cast<int *>(smem + S::kU) + warp * kStages;
-  DecodeJoin join{0, 0, 0, 0, 0};
+  DecodeJoin join{};
 
   DecCursor cursor = cursor_begin(st), here;
   DecBatch d;
@@ -288,15 +306,14 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
         acc.w += x.w * f;
       }
       if (whole) {
-        write_row<T>(p, d, v, b, hh, r, c, acc, mm, ll);
+        write_row<T>(p, d.q.tok0, p.cu_q ? 0 : b, hh, v.t0, v.first + r, c, acc, mm, ll);
       } else {
         reinterpret_cast<float4 *>(p.part_o + (int64_t(slot) * kTile + r) * D)[c] = acc;
         if (c == 0) reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * kTile + r] = make_float2(mm, ll);
       }
     }
     __syncthreads();
-    if (cs == 0 && !whole)
-      join = {b, hh, tile, int(dec_owner(here.pos + d.chunks - 1, st.total, st.blocks) - blockIdx.x) + 1, slot};
+    if (cs == 0 && !whole) join = dec_join(p, st, here, d, seg, v, slot);
   }
   __shared__ uint32_t s_flags;
   if (tid == 0) s_flags = 0;
@@ -310,69 +327,107 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
 }
 
 // Joins the parts of the unit that attention block blockIdx.x began and did
-// not finish: a warp per row, a lane per D / 32 columns.
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) k_decode_join(const DecodeProblem p) {
+// not finish.  A warp takes a row, or, where the block has more warps than
+// rows, every wpr-th part of it; a part's state and output are requested
+// together, four parts at a time.
+template <int D, typename T, int kJoinWarps>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_decode_join(const DecodeProblem p) {
+  __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   griddep_wait();
   griddep_launch_next();
+  const DecodeJoin j = p.join[blockIdx.x];
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     __shared__ uint32_t s_flags;
     if (threadIdx.x == 0) s_flags = 0;
     __syncthreads();
     uint32_t f = 0;
-    for (int i = threadIdx.x; i < p.grid; i += kThreads) f |= p.flags[i];
+    for (int i = threadIdx.x; i < p.grid; i += 32 * kJoinWarps) f |= p.flags[i];
     if (f) atomicOr(&s_flags, f);
     __syncthreads();
     if (threadIdx.x < kStWords) p.status[threadIdx.x] = threadIdx.x == kStFlags ? s_flags : 0;
   }
-  const DecodeJoin j = p.join[blockIdx.x];
-  if (j.parts == 0) return;
-  const int lane = threadIdx.x & 31, r = int(blockIdx.y) * kWarps + (threadIdx.x >> 5);
-  uint32_t ignore = 0;
-  const DecBatch d = dec_batch(p, j.b, ignore);
-  const DecRows v = dec_rows(p, d, j.tile);
-  if (r >= v.rows) return;
-  // part 0 in slot0, part i at the beginning of block blockIdx.x + i
-  auto slot = [&](int i) { return int64_t(i == 0 ? j.slot0 : 2 * (int(blockIdx.x) + i)) * p.TR + r; };
-  const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml);
-  float m = -INFINITY;
-  for (int i = lane; i < j.parts; i += 32) m = fmaxf(m, ml[slot(i)].x);
+  const int r0 = int(blockIdx.y) * kJoinWarps, rows = min(kJoinWarps, j.rows - r0);
+  if (j.parts == 0 || rows <= 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int wpr = 1;
+  while (2 * wpr * rows <= kJoinWarps) wpr *= 2;
+  const int row = warp / wpr, phase = warp % wpr, r = r0 + row;
+  constexpr int kC = D / 32, kBatch = 4;
+  float m = -INFINITY, l = 0.f, acc[kC];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[D / 32];
+  for (int c = 0; c < kC; ++c) acc[c] = 0.f;
+  if (row < rows) {
+    // part 0 in slot0, part i at the beginning of the i-th group of blocks after this one's
+    for (int i0 = phase; i0 < j.parts; i0 += wpr * kBatch) {
+      float2 ml[kBatch];
+      float o[kBatch][kC];
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < j.parts; ++i) {
-    const float2 x = ml[slot(i)];
-    const float f = ex2(x.x - ref);
-    const float *o = p.part_o + slot(i) * D + lane * (D / 32);
-    l += x.y * f;
-    if constexpr (D == 128) {
-      const float4 y = *reinterpret_cast<const float4 *>(o);
-      acc[0] += y.x * f;
-      acc[1] += y.y * f;
-      acc[2] += y.z * f;
-      acc[3] += y.w * f;
-    } else {
-      const float2 y = *reinterpret_cast<const float2 *>(o);
-      acc[0] += y.x * f;
-      acc[1] += y.y * f;
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * wpr;
+        if (i < j.parts) {
+          const int64_t at = int64_t(i == 0 ? j.slot0 : 2 * (int(blockIdx.x) + i * p.group)) * p.TR + r;
+          ml[k] = reinterpret_cast<const float2 *>(p.part_ml)[at];
+          const float *src = p.part_o + at * D + lane * kC;
+          if constexpr (kC == 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(src);
+            o[k][0] = y.x; o[k][1] = y.y; o[k][2] = y.z; o[k][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2 *>(src);
+            o[k][0] = y.x; o[k][1] = y.y;
+          }
+        } else {
+          ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int c = 0; c < kC; ++c) o[k][c] = 0.f;
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+      const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - ref);
+      l *= f0;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) acc[c] *= f0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float f = ex2(ml[k].x - ref);
+        l += ml[k].y * f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) acc[c] += o[k][c] * f;
+      }
+      m = mn;
     }
   }
+  if (wpr > 1) {  // the same for every warp of the block
+#pragma unroll
+    for (int c = 0; c < kC; ++c) s_o[warp][lane * kC + c] = acc[c];
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+    __syncthreads();
+    if (phase != 0) return;
+    for (int w = 1; w < wpr; ++w) {
+      const float mw = s_m[warp + w], mn = fmaxf(m, mw);
+      const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - ref), f1 = ex2(mw - ref);
+      l = l * f0 + s_l[warp + w] * f1;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) acc[c] = acc[c] * f0 + s_o[warp + w][lane * kC + c] * f1;
+      m = mn;
+    }
+  }
+  if (row >= rows) return;
   if constexpr (D == 128) {
-    write_row<T>(p, d, v, j.b, j.hh, r, lane, make_float4(acc[0], acc[1], acc[2], acc[3]), m, l);
+    write_row<T>(p, j.tok0, j.b, j.hh, j.t0, j.first + r, lane, make_float4(acc[0], acc[1], acc[2], acc[3]), m, l);
   } else {
     const float a = __shfl_down_sync(0xffffffffu, acc[0], 1), c = __shfl_down_sync(0xffffffffu, acc[1], 1);
-    if ((lane & 1) == 0) write_row<T>(p, d, v, j.b, j.hh, r, lane / 2, make_float4(acc[0], acc[1], a, c), m, l);
+    if ((lane & 1) == 0)
+      write_row<T>(p, j.tok0, j.b, j.hh, j.t0, j.first + r, lane / 2, make_float4(acc[0], acc[1], a, c), m, l);
   }
 }
 
 template <int D, typename T>
 cudaError_t launch_join(const DecodeProblem &p, cudaStream_t s) {
-  return launch_dep(k_decode_join<D, T>, dim3(unsigned(p.grid), unsigned((p.TR + kWarps - 1) / kWarps)),
-                    dim3(kThreads), 0, s, p);
+  // few rows: one block a unit, so that its warps can share the parts of a row
+  if (p.TR == kTile) return launch_dep(k_decode_join<D, T, kTile>, dim3(unsigned(p.grid)), dim3(32 * kTile), 0, s, p);
+  return launch_dep(k_decode_join<D, T, 8>, dim3(unsigned(p.grid), unsigned(p.TR / 8)), dim3(256), 0, s, p);
 }
 
 template <int D, typename T, int kMask>
@@ -398,6 +453,7 @@ void decode_plan(DecodeProblem &p) {
   if (tokens * p.gg > kFewRows) return decode_tc_plan(p);
   p.TR = kTile;
   p.chunk = kChunk;
+  p.group = 1;
   p.grid = num_sms() * (p.D == 128 ? 2 : 4);
 }
 

@@ -39,6 +39,7 @@ constexpr int kSBufs = 3;
 constexpr int kKWarp = 8, kPvWarp = 9, kVWarp = 10, kSWarp = 11;
 constexpr int kCols = 64;  // kv columns of a softmax thread
 constexpr float kRescaleSum = 256.0f;
+constexpr int kMostGroup = 8;  // larger groups leave more SMs without a group
 constexpr int kReaders = 11;  // warps that read the chunk lists
 
 // up to 32 chunks of a segment, those that hold tokens
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const DecStart st = dec_start<kThreads>(p, *reinterpret_cast<DecScratch<kThreads> *>(smem_raw + L::kXsum), len_flags);
   if (tid == 0) {
     *status = base & 1023u ? BSA_FLAG_INTERNAL : 0u;  // swizzled tiles need a 1024-byte aligned base
-    p.join[blockIdx.x] = DecodeJoin{0, 0, 0, 0, 0};
+    p.join[blockIdx.x] = DecodeJoin{};
     __threadfence();
   }
   __syncthreads();
@@ -499,9 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (wg == 0) reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * kTile + r] = make_float2(m, lsum);
         }
       }
-      if (tid == 0 && seg.cs == 0 && !whole)
-        p.join[blockIdx.x] = {here.b, seg.hh, seg.tile,
-                              int(dec_owner(here.pos + d.chunks - 1, st.total, st.blocks) - blockIdx.x) + 1, slot};
+      if (tid == 0 && seg.cs == 0 && !whole) p.join[blockIdx.x] = dec_join(p, st, here, d, seg, v, slot);
       tc_fence_before();
       ++seg_n;
     }
@@ -528,7 +527,13 @@ cudaError_t launch(const DecodeProblem &p, const CUtensorMap &k, const CUtensorM
 void decode_tc_plan(DecodeProblem &p) {
   p.TR = kTile;
   p.chunk = kChunk;
-  p.grid = num_sms();
+  // as many blocks side by side as a sequence of the mean number of tokens
+  // has tiles (sparse: tiles of one query block, which share an index row)
+  const int64_t tokens = p.q_layout == BSA_LAYOUT_BNSD ? p.Sq : (p.Tq + p.B - 1) / p.B;
+  const int64_t rows = (p.index && tokens > p.BQ ? p.BQ : tokens) * p.gg;
+  const int64_t tiles = (rows + kTile - 1) / kTile;
+  p.group = int32_t(tiles < kMostGroup ? tiles : kMostGroup);
+  p.grid = num_sms() / p.group * p.group;
 }
 
 cudaError_t launch_decode_tc(const DecodeProblem &p, cudaStream_t s) {
