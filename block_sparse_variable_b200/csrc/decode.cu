@@ -326,6 +326,19 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
   }
 }
 
+// the attention blocks' flags into the status word, by one block
+template <int kN>
+__device__ void join_flags(const DecodeProblem &p) {
+  __shared__ uint32_t s_flags;
+  if (threadIdx.x == 0) s_flags = 0;
+  __syncthreads();
+  uint32_t f = 0;
+  for (int i = threadIdx.x; i < p.grid; i += kN) f |= p.flags[i];
+  if (f) atomicOr(&s_flags, f);
+  __syncthreads();
+  if (threadIdx.x < kStWords) p.status[threadIdx.x] = threadIdx.x == kStFlags ? s_flags : 0;
+}
+
 // Joins the parts of the unit that attention block blockIdx.x began and did
 // not finish.  A warp takes a row, or, where the block has more warps than
 // rows, every wpr-th part of it; a part's state and output are requested
@@ -336,27 +349,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_decode_join(const DecodePro
   griddep_wait();
   griddep_launch_next();
   const DecodeJoin j = p.join[blockIdx.x];
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    __shared__ uint32_t s_flags;
-    if (threadIdx.x == 0) s_flags = 0;
-    __syncthreads();
-    uint32_t f = 0;
-    for (int i = threadIdx.x; i < p.grid; i += 32 * kJoinWarps) f |= p.flags[i];
-    if (f) atomicOr(&s_flags, f);
-    __syncthreads();
-    if (threadIdx.x < kStWords) p.status[threadIdx.x] = threadIdx.x == kStFlags ? s_flags : 0;
-  }
-  const int r0 = int(blockIdx.y) * kJoinWarps, rows = min(kJoinWarps, j.rows - r0);
-  if (j.parts == 0 || rows <= 0) return;
+  if (blockIdx.x == 0) join_flags<32 * kJoinWarps>(p);
+  const int rows = j.rows;  // at most kJoinWarps
+  if (j.parts == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int wpr = 1;
   while (2 * wpr * rows <= kJoinWarps) wpr *= 2;
-  const int row = warp / wpr, phase = warp % wpr, r = r0 + row;
+  const int r = warp / wpr, phase = warp % wpr;
   constexpr int kC = D / 32, kBatch = 4;
   float m = -INFINITY, l = 0.f, acc[kC];
 #pragma unroll
   for (int c = 0; c < kC; ++c) acc[c] = 0.f;
-  if (row < rows) {
+  if (r < rows) {
     // part 0 in slot0, part i at the beginning of the i-th group of blocks after this one's
     for (int i0 = phase; i0 < j.parts; i0 += wpr * kBatch) {
       float2 ml[kBatch];
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_decode_join(const DecodePro
       m = mn;
     }
   }
-  if (row >= rows) return;
+  if (r >= rows) return;
   if constexpr (D == 128) {
     write_row<T>(p, j.tok0, j.b, j.hh, j.t0, j.first + r, lane, make_float4(acc[0], acc[1], acc[2], acc[3]), m, l);
   } else {
@@ -423,11 +427,55 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_decode_join(const DecodePro
   }
 }
 
+// The same for the parts of 128-row tiles, which hold four columns of all rows
+// side by side: eight rows a block, a thread four columns of one.
+template <int D, typename T>
+__global__ void __launch_bounds__(2 * D) k_decode_join_tiles(const DecodeProblem p) {
+  griddep_wait();
+  griddep_launch_next();
+  const DecodeJoin j = p.join[blockIdx.x];
+  if (blockIdx.x == 0 && blockIdx.y == 0) join_flags<2 * D>(p);
+  const int r = int(blockIdx.y) * 8 + int(threadIdx.x & 7), c = int(threadIdx.x >> 3);
+  if (j.parts == 0 || r >= j.rows) return;
+  constexpr int kBatch = 4;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < j.parts; i0 += kBatch) {
+    float2 ml[kBatch];
+    float4 o[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < j.parts) {
+        const int64_t at = i == 0 ? j.slot0 : 2 * (int(blockIdx.x) + i * p.group);
+        ml[k] = reinterpret_cast<const float2 *>(p.part_ml)[at * p.TR + r];
+        o[k] = reinterpret_cast<const float4 *>(p.part_o)[(at * (D / 4) + c) * p.TR + r];
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - ref);
+    l *= f0;
+    acc.x *= f0; acc.y *= f0; acc.z *= f0; acc.w *= f0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float f = ex2(ml[k].x - ref);
+      l += ml[k].y * f;
+      acc.x += o[k].x * f; acc.y += o[k].y * f; acc.z += o[k].z * f; acc.w += o[k].w * f;
+    }
+    m = mn;
+  }
+  write_row<T>(p, j.tok0, j.b, j.hh, j.t0, j.first + r, c, acc, m, l);
+}
+
 template <int D, typename T>
 cudaError_t launch_join(const DecodeProblem &p, cudaStream_t s) {
   // few rows: one block a unit, so that its warps can share the parts of a row
   if (p.TR == kTile) return launch_dep(k_decode_join<D, T, kTile>, dim3(unsigned(p.grid)), dim3(32 * kTile), 0, s, p);
-  return launch_dep(k_decode_join<D, T, 8>, dim3(unsigned(p.grid), unsigned(p.TR / 8)), dim3(256), 0, s, p);
+  return launch_dep(k_decode_join_tiles<D, T>, dim3(unsigned(p.grid), unsigned(p.TR / 8)), dim3(2 * D), 0, s, p);
 }
 
 template <int D, typename T, int kMask>

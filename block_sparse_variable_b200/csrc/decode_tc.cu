@@ -2,16 +2,26 @@
 // query rows (draft trees and chains: tokens times the heads of a group).
 //
 // Math, division of the work and joining of parts: decode.cu, decode_plan.cuh.
-// The pipeline is the forward pass's: one block per SM, TMA loads of 128-token
-// chunks of K and V through three-stage rings (warps 8 and 10), S = Q K^T and
-// O += P V issued by warps 11 and 9, two softmax warpgroups on the two column
-// halves of S with a reference maximum that moves only when a half-row sum
-// passes 2^8.  Here the rows of a tile are gathered (any number of heads and
-// tokens) by the softmax threads.  Only warp 8 walks the index and the block
-// table: it publishes the chunks of a segment 32 at a time in shared memory,
-// and the other warps read them there (a walk of their own cost the softmax
-// threads 40 registers, spilled).  A chunk that reaches the masked tokens or
-// the end of the cache gets a 64-bit visibility word per row and half.
+//
+// One block per SM.  TMA loads of 128-token chunks of K and V through
+// three-stage rings (warps 8 and 10); S = Q K^T and O += P V issued by warps 11
+// and 9; two softmax warpgroups that take the chunks in turn, a thread a whole
+// row of 128 scores, each with a running maximum, sum and output of its own.
+// Nothing in the loop passes between the two groups, and while one waits for
+// its products the other has the exponentials to itself; their states are
+// joined at the end of a segment.  (Two groups on the column halves of the
+// same chunk, as in the forward pass, met once a chunk: 2640 clocks a chunk
+// against about 1050 of products and 1024 of exponentials.)  TMEM holds two
+// S / P buffers and two outputs: all 512 columns at D = 128.
+//
+// The rows of a tile are gathered (any number of heads and tokens) by the
+// softmax threads, the next segment's before the epilogue of the one before.
+// Only warp 8, which runs ahead, follows the division of the work and walks
+// the index and the block table: it publishes segments and their chunks, 32 at
+// a time, in shared memory.  (Under a loaded memory system a dependent load
+// costs 2000 to 3000 clocks; with every warp following the plan by itself a
+// change of segments took 38000.)  A chunk that reaches the masked tokens or
+// the end of the cache gets 64-bit visibility words per row.
 //
 // Bound by memory up to about 128 rows of a kv head, by the tensor pipe and
 // the exponentials above.
@@ -20,6 +30,7 @@
 
 #include "cache.h"
 #include "decode_plan.cuh"
+#include "f32x2.cuh"
 #include "launch.cuh"
 #include "pack16.cuh"
 #include "sm100.cuh"
@@ -35,36 +46,44 @@ constexpr int kTile = 128, kChunk = 128;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kStages = 3;
-constexpr int kSBufs = 3;
 constexpr int kKWarp = 8, kPvWarp = 9, kVWarp = 10, kSWarp = 11;
-constexpr int kCols = 64;  // kv columns of a softmax thread
-constexpr float kRescaleSum = 256.0f;
+// a row's reference maximum moves once a score passes it by 2^8: weights stay
+// below 2^8, and the output is rarely rescaled
+constexpr float kSlack = 8.0f;
 constexpr int kMostGroup = 8;  // larger groups leave more SMs without a group
 constexpr int kReaders = 11;  // warps that read the chunk lists
 
+// a segment as the reading warps need it
+struct SegInfo {
+  int b, tok0;            // BNSD sequence (0 when packed), first query row
+  int kv_b, kv_tok0, h2;  // where K and V are
+  int kvlen, qlen;
+  int hh, t0, first, rows;  // decode_plan.cuh: DecSeg, DecRows
+  int slot;               // of the workspace; -1: the unit is finished here
+};
 // up to 32 chunks of a segment, those that hold tokens
 struct ChunkList {
-  int n, last;  // last: the segment ends with this list
+  int n, last;  // last: the segment ends with this list; n < 0: no more segments
   int u[32], page[32];
+  SegInfo seg;
 };
 
 enum : int {
-  kBarQFull = 0,    // one arrival per softmax thread
-  kBarKFull = 1,    // + K stage
-  kBarKEmpty = 4,   // + K stage
-  kBarVFull = 7,    // + V stage
-  kBarVEmpty = 10,  // + V stage
-  kBarSFull = 13,   // + S buffer
-  kBarPFull = 16,   // + S buffer (one arrival per softmax thread)
-  kBarPVDone = 19,  // + (chunk index & 1)
-  kBarXchg = 21,    // + row quarter
-  kBarDrain = 25,
-  kBarSFree = 26,   // + S buffer
+  kBarQFull = 0,       // one arrival per softmax thread
+  kBarQEmpty = 1,      // the segment's last S has read Q
+  kBarKFull = 2,       // + K stage
+  kBarKEmpty = 5,      // + K stage
+  kBarVFull = 8,       // + V stage
+  kBarVEmpty = 11,     // + V stage
+  kBarSFull = 14,      // + group
+  kBarPFull = 16,      // + group (one arrival per thread of the group)
+  kBarPVDone = 18,     // + group: P V is in O, and the S / P buffer is free
+  kBarXchg = 20,       // + row quarter: rendezvous of the warps on the same 32 rows
+  kBarListFull = 24,   // + list buffer
+  kBarListEmpty = 26,  // + list buffer (one arrival per reading warp)
+  kBarDrain = 28,
   kBarDrainS = 29,
-  kBarQEmpty = 30,  // the segment's last S has read Q
-  kBarListFull = 31,   // + list buffer
-  kBarListEmpty = 33,  // + list buffer (one arrival per reading warp)
-  kNumBars = 35
+  kNumBars = 30
 };
 
 template <int D>
@@ -75,14 +94,13 @@ struct Layout {
   static constexpr int kK = kQ + kTileBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
   static constexpr int kBars = kV + kStages * kTileBytes;
-  static constexpr int kFlags = kBars + kNumBars * 8;     // [2][8 softmax warps] u32
-  static constexpr int kXsum = kFlags + 2 * 8 * 4;        // [2][128] half-row sums
-  static constexpr int kLists = kXsum + 2 * 128 * 4;      // [2] ChunkList
+  static constexpr int kMl = kBars + kNumBars * 8;        // [2 groups][128] maximum and sum
+  static constexpr int kLists = kMl + 2 * 128 * 8;        // [2] ChunkList
   static constexpr int kBlk = kLists + 2 * int(sizeof(ChunkList));  // [32] ints of the walking warp
   static constexpr int kTmemPtr = kBlk + 128;
   static constexpr int kAbort = kTmemPtr + 4;
   static constexpr int kBytes = kAbort + 4;
-  static_assert(kXsum % 8 == 0 && sizeof(DecScratch<kThreads>) <= 1024, "the plan's scratch");
+  static_assert(kMl % 8 == 0 && sizeof(DecScratch<kThreads>) <= 2048, "the plan's scratch");
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -110,9 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *status = p.flags + blockIdx.x;  // this block's flags
   const uint32_t base = smem_u32(smem_raw);
   uint32_t len_flags = 0;
-  // (the row sums' memory serves as scratch here; nothing is in static shared
+  // (the states' memory serves as scratch here; nothing is in static shared
   // memory, so that the tiles start at the 1024-byte aligned window)
-  const DecStart st = dec_start<kThreads>(p, *reinterpret_cast<DecScratch<kThreads> *>(smem_raw + L::kXsum), len_flags);
+  const DecStart st = dec_start<kThreads>(p, *reinterpret_cast<DecScratch<kThreads> *>(smem_raw + L::kMl), len_flags);
   if (tid == 0) {
     *status = base & 1023u ? BSA_FLAG_INTERNAL : 0u;  // swizzled tiles need a 1024-byte aligned base
     p.join[blockIdx.x] = DecodeJoin{};
@@ -136,13 +154,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarVFull + s), 1);
       mbar_init(bar(kBarVEmpty + s), 1);
     }
-    for (int b = 0; b < kSBufs; ++b) {
-      mbar_init(bar(kBarSFull + b), 1);
-      mbar_init(bar(kBarPFull + b), kSoftmaxThreads);
-      mbar_init(bar(kBarSFree + b), 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(kBarSFull + g), 1);
+      mbar_init(bar(kBarPFull + g), 128);
+      mbar_init(bar(kBarPVDone + g), 1);
     }
-    mbar_init(bar(kBarPVDone), 1);
-    mbar_init(bar(kBarPVDone + 1), 1);
     for (int q = 0; q < 4; ++q) mbar_init(bar(kBarXchg + q), kSoftmaxThreads / 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarListFull + i), 1);
@@ -161,15 +177,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS0 = tmem, tO = tmem + uint32_t(kSBufs) * 128u;
+  const uint32_t tS0 = tmem, tO0 = tmem + 256u;
 
-  DecCursor cursor = cursor_begin(st), here{};
-  DecBatch d{};
-  DecSeg seg{};
-  uint32_t kv_it = 0;
+  uint32_t kv_it = 0, list_it = 0;
   bool ok = true;
-
-  uint32_t list_it = 0;
+  // the list that begins the next segment, or null at the end
+  auto next_segment = [&]() -> const volatile ChunkList * {
+    const int i = int(list_it & 1u);
+    ok = ok && wait_warp(bar(kBarListFull + i), (list_it >> 1) & 1u, abort, status);
+    return ok && lists[i].n >= 0 ? lists + i : nullptr;
+  };
   // f(first token, page) for every chunk of the segment, by a reading warp
   auto each_chunk = [&](auto &&f) {
     for (bool last = false; ok && !last; ++list_it) {
@@ -183,134 +200,169 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  if (warp == kKWarp || warp == kVWarp) {
-    // ----------------------------------------------------- TMA producers
-    const bool is_k = warp == kKWarp;
-    const CUtensorMap *map = is_k ? &map_k : &map_v;
-    if (lane == 0) tma_prefetch_desc(map);
-    const uint32_t ring = is_k ? sK : sV;
-    const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
-    int armed[kStages] = {-1, -1, -1};
-    uint32_t flags = 0;
-    auto load = [&](int u, int pg, int h2) {
-      const int s = int(kv_it % kStages);
-      const uint32_t ph = (kv_it / kStages) & 1u;
-      if (!(ok = wait_warp(bar(empty0 + s), ph ^ 1u, abort, status))) return;
-      if (lane == 0) {
-        int row, last;  // tile coordinates: (0, row, 0, h2, last)
-        if (p.kv.table) { row = u % p.kv.page_size; last = pg; }
-        else if (p.kv.cu_kv) { row = int(d.kv.tok0) + u; last = 0; }
-        else { row = u; last = here.b; }
-        mbar_expect_tx(bar(full0 + s), L::kTileBytes);
-        tma_load_5d(ring + s * L::kTileBytes, map, bar(full0 + s), 0, row, 0, h2, last);
-      }
-      armed[s] = int(ph);
-      ++kv_it;
-    };
-    while (ok && cursor_next(p, st, cursor, d, seg, here)) {
-      const int h2 = seg.hh / (p.H / p.N2);
-      if (is_k) {
-        DecWalk w = walk_begin(p, here.b, seg.hh, dec_rows(p, d, seg.tile).irow, here.qoff);
-        int *blk = reinterpret_cast<int *>(smem_raw + L::kBlk);
-        for (int x = seg.cs & ~31; x < seg.ce && ok; x += 32, ++list_it) {
-          int u, pg;
-          walk_fetch(p, d, here.b, w, x, seg.ce, blk, lane, u, pg);
-          const uint32_t some = __ballot_sync(0xffffffffu, u >= 0 && x + lane >= seg.cs);
-          const int n = __popc(some), i = int(list_it & 1u);
-          if (!(ok = wait_warp(bar(kBarListEmpty + i), ((list_it >> 1) & 1u) ^ 1u, abort, status))) break;
-          if (some >> lane & 1u) {
-            const int at = __popc(some & ((1u << lane) - 1u));
-            lists[i].u[at] = u;
-            lists[i].page[at] = pg;
-          }
-          if (lane == 0) {
-            lists[i].n = n;
-            lists[i].last = x + 32 >= seg.ce;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarListFull + i));
-          for (int c = 0; c < n && ok; ++c) load(lists[i].u[c], lists[i].page[c], h2);
+  // registers: the softmax threads hold a row of 128 scores (256 x 216 + 128 x
+  // 72 = the 384 x 168 of the launch)
+  if (warp >= 8) {
+    regs_dec<72>();
+    if (warp == kKWarp || warp == kVWarp) {
+      // --------------------------------------------------- TMA producers
+      const bool is_k = warp == kKWarp;
+      const CUtensorMap *map = is_k ? &map_k : &map_v;
+      if (lane == 0) tma_prefetch_desc(map);
+      const uint32_t ring = is_k ? sK : sV;
+      const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
+      int armed[kStages] = {-1, -1, -1};
+      auto load = [&](int u, int pg, const volatile SegInfo &g) {
+        const int s = int(kv_it % kStages);
+        const uint32_t ph = (kv_it / kStages) & 1u;
+        if (!(ok = wait_warp(bar(empty0 + s), ph ^ 1u, abort, status))) return;
+        if (lane == 0) {
+          int row, last;  // tile coordinates: (0, row, 0, h2, last)
+          if (p.kv.table) { row = u % p.kv.page_size; last = pg; }
+          else if (p.kv.cu_kv) { row = g.kv_tok0 + u; last = 0; }
+          else { row = u; last = g.kv_b; }
+          mbar_expect_tx(bar(full0 + s), L::kTileBytes);
+          tma_load_5d(ring + s * L::kTileBytes, map, bar(full0 + s), 0, row, 0, g.h2, last);
         }
-        flags |= w.flags;
-      } else {
-        each_chunk([&](int u, int pg) { load(u, pg, h2); });
-      }
-    }
-    if (*abort && lane == 0) {  // let every copy already issued land before the block exits
-      for (int s = 0; s < kStages; ++s)
-        if (armed[s] >= 0) drain_wait(bar(full0 + s), uint32_t(armed[s]));
-    }
-    if (is_k && flags) atomicOr(status, flags);
-    __syncwarp();
-  } else if (warp == kPvWarp || warp == kSWarp) {
-    // -------------------------------------------------------- MMA issuers
-    constexpr uint32_t idS = idesc_f16(BF16, 128, 128, false, false);
-    constexpr uint32_t idPV = idesc_f16(BF16, 128, D, false, true);
-    const uint64_t dQ = sw128_desc(sQ, 16, 1024);
-    const uint64_t dK = sw128_desc(sK, 16, 1024);
-    const uint64_t dV = sw128_desc(sV, L::kBox, 1024);
-    auto kstep = [](int kk) { return uint64_t((kk >> 2) * (L::kBox >> 4) + (kk & 3) * 2); };
-    // P of the first 64 kv columns in TMEM columns [0, 32) of the S buffer, of the next 64 in [64, 96)
-    auto pcol = [](int kk) { return uint32_t(64 * (kk >> 2) + 8 * (kk & 3)); };
-    const bool is_s = warp == kSWarp;
-    uint32_t q_it = 0;
-    while (ok && cursor_next(p, st, cursor, d, seg, here)) {
-      if (is_s) {
-        // Q is written for every segment, whether or not it has a chunk
-        if (!(ok = wait_warp(bar(kBarQFull), q_it & 1u, abort, status))) break;
-        ++q_it;
-        each_chunk([&](int, int) {
-          const uint32_t t = kv_it;
-          const int b = int(t % kSBufs), sg = int(t % kStages);
-          if (t >= uint32_t(kSBufs) && !(ok = wait_warp(bar(kBarSFree + b), (t / kSBufs - 1) & 1u, abort, status)))
-            return;
-          if (!(ok = wait_warp(bar(kBarKFull + sg), (t / kStages) & 1u, abort, status))) return;
-          tc_fence_after();
-          const uint32_t da = tS0 + uint32_t(b) * 128u;
-          const uint64_t ka = dK + uint64_t(sg * (L::kTileBytes >> 4));
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) mma_ss_e(da, dQ + kstep(kk), ka + kstep(kk), idS, kk > 0 ? 1u : 0u);
-          mma_commit_e(bar(kBarSFull + b));
-          mma_commit_e(bar(kBarKEmpty + sg));
-          ++kv_it;
-        });
-        if (!ok) break;
-        mma_commit_e(bar(kBarQEmpty));
-      } else {
-        uint32_t acc = 0;
-        each_chunk([&](int, int) {
-          const uint32_t t = kv_it;
-          const int b = int(t % kSBufs), sg = int(t % kStages);
-          if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
-          if (!(ok = wait_warp(bar(kBarPFull + b), (t / kSBufs) & 1u, abort, status))) return;
-          tc_fence_after();
-          const uint32_t pa = tS0 + uint32_t(b) * 128u;
-          const uint64_t vd = dV + uint64_t(sg * (L::kTileBytes >> 4));
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            mma_ts_e(tO, pa + pcol(kk), vd + uint64_t(kk * 128), idPV, acc);
-            acc = 1;
+        armed[s] = int(ph);
+        ++kv_it;
+      };
+      if (is_k) {
+        uint32_t flags = 0;
+        DecCursor cursor = cursor_begin(st), here;
+        DecBatch d;
+        DecSeg seg;
+        int *blk = reinterpret_cast<int *>(smem_raw + L::kBlk);
+        while (ok && cursor_next(p, st, cursor, d, seg, here)) {
+          const DecRows v = dec_rows(p, d, seg.tile);
+          const bool whole = seg.cs == 0 && seg.ce == d.chunks;
+          const int slot = here.pos == st.lo ? 2 * int(blockIdx.x) : 2 * int(blockIdx.x) + 1;
+          if (lane == 0 && seg.cs == 0 && !whole) p.join[blockIdx.x] = dec_join(p, st, here, d, seg, v, slot);
+          // the tile's query rows into L2, ahead of their gathering
+          for (int r = lane; r < v.rows; r += 32) {
+            const int y = v.first + r;
+            const T *q = static_cast<const T *>(p.q) + (p.cu_q ? 0 : here.b) * p.q_sb +
+                         (d.q.tok0 + v.t0 + y / p.gg) * p.q_st + int64_t(seg.hh * p.gg + y % p.gg) * p.q_sh;
+            asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q));
+            asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q + D - 8));
           }
-          mma_commit_e(bar(kBarPVDone + int(t & 1u)));
-          mma_commit_e(bar(kBarVEmpty + sg));
-          mma_commit_e(bar(kBarSFree + b));
-          ++kv_it;
-        });
+          DecWalk w = walk_begin(p, here.b, seg.hh, v.irow, here.qoff);
+          for (int x = seg.cs & ~31; x < seg.ce && ok; x += 32, ++list_it) {
+            int u, pg;
+            walk_fetch(p, d, here.b, w, x, seg.ce, blk, lane, u, pg);
+            const uint32_t some = __ballot_sync(0xffffffffu, u >= 0 && x + lane >= seg.cs);
+            const int n = __popc(some), i = int(list_it & 1u);
+            if (!(ok = wait_warp(bar(kBarListEmpty + i), ((list_it >> 1) & 1u) ^ 1u, abort, status))) break;
+            volatile ChunkList &list = lists[i];
+            if (some >> lane & 1u) {
+              const int at = __popc(some & ((1u << lane) - 1u));
+              list.u[at] = u;
+              list.page[at] = pg;
+            }
+            if (lane == 0) {
+              list.n = n;
+              list.last = x + 32 >= seg.ce;
+              volatile SegInfo &g = list.seg;
+              g.b = p.cu_q ? 0 : here.b; g.tok0 = int(d.q.tok0);
+              g.kv_b = here.b; g.kv_tok0 = int(d.kv.tok0); g.h2 = seg.hh / (p.H / p.N2);
+              g.kvlen = d.kv.kvlen; g.qlen = d.q.qlen;
+              g.hh = seg.hh; g.t0 = v.t0; g.first = v.first; g.rows = v.rows;
+              g.slot = whole ? -1 : slot;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarListFull + i));
+            for (int c = 0; c < n && ok; ++c) load(list.u[c], list.page[c], list.seg);
+          }
+          flags |= w.flags;
+        }
+        const int i = int(list_it & 1u);
+        if (ok && (ok = wait_warp(bar(kBarListEmpty + i), ((list_it >> 1) & 1u) ^ 1u, abort, status))) {
+          if (lane == 0) {
+            lists[i].n = -1;
+            mbar_arrive(bar(kBarListFull + i));
+          }
+        }
+        if (flags) atomicOr(status, flags);
+      } else {
+        while (const volatile ChunkList *list = next_segment()) {
+          SegInfo g{};
+          g.kv_b = list->seg.kv_b; g.kv_tok0 = list->seg.kv_tok0; g.h2 = list->seg.h2;
+          each_chunk([&](int u, int pg) { load(u, pg, g); });
+        }
       }
+      if (*abort && lane == 0) {  // let every copy already issued land before the block exits
+        for (int s = 0; s < kStages; ++s)
+          if (armed[s] >= 0) drain_wait(bar(full0 + s), uint32_t(armed[s]));
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------ MMA issuers
+      constexpr uint32_t idS = idesc_f16(BF16, 128, 128, false, false);
+      constexpr uint32_t idPV = idesc_f16(BF16, 128, D, false, true);
+      const uint64_t dQ = sw128_desc(sQ, 16, 1024);
+      const uint64_t dK = sw128_desc(sK, 16, 1024);
+      const uint64_t dV = sw128_desc(sV, L::kBox, 1024);
+      auto kstep = [](int kk) { return uint64_t((kk >> 2) * (L::kBox >> 4) + (kk & 3) * 2); };
+      if (warp == kSWarp) {
+        for (uint32_t q_it = 0; next_segment(); ++q_it) {
+          if (!(ok = wait_warp(bar(kBarQFull), q_it & 1u, abort, status))) break;
+          each_chunk([&](int, int) {
+            const uint32_t t = kv_it, g = t & 1u;
+            const int sg = int(t % kStages);
+            if (t >= 2 && !(ok = wait_warp(bar(kBarPVDone + g), (t / 2 - 1) & 1u, abort, status))) return;
+            if (!(ok = wait_warp(bar(kBarKFull + sg), (t / kStages) & 1u, abort, status))) return;
+            tc_fence_after();
+            const uint32_t da = tS0 + g * 128u;
+            const uint64_t ka = dK + uint64_t(sg * (L::kTileBytes >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) mma_ss_e(da, dQ + kstep(kk), ka + kstep(kk), idS, kk > 0 ? 1u : 0u);
+            mma_commit_e(bar(kBarSFull + g));
+            mma_commit_e(bar(kBarKEmpty + sg));
+            ++kv_it;
+          });
+          if (!ok) break;
+          mma_commit_e(bar(kBarQEmpty));
+        }
+      } else {
+        while (next_segment()) {
+          uint32_t acc[2] = {0, 0};
+          each_chunk([&](int, int) {
+            const uint32_t t = kv_it, g = t & 1u;
+            const int sg = int(t % kStages);
+            if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
+            if (!(ok = wait_warp(bar(kBarPFull + g), (t / 2) & 1u, abort, status))) return;
+            tc_fence_after();
+            const uint32_t pa = tS0 + g * 128u, da = tO0 + g * uint32_t(D);  // 16 kv rows of P are 8 columns
+            const uint64_t vd = dV + uint64_t(sg * (L::kTileBytes >> 4));
+            uint32_t on = g ? acc[1] : acc[0];
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              mma_ts_e(da, pa + uint32_t(8 * kk), vd + uint64_t(kk * 128), idPV, on);
+              on = 1;
+            }
+            if (g) acc[1] = 1;
+            else acc[0] = 1;
+            mma_commit_e(bar(kBarPVDone + g));
+            mma_commit_e(bar(kBarVEmpty + sg));
+            ++kv_it;
+          });
+        }
+      }
+      if (*abort) {  // let issued MMAs finish before TMEM is freed
+        const int dr = warp == kSWarp ? kBarDrainS : kBarDrain;
+        mma_commit_e(bar(dr));
+        if (lane == 0) drain_wait(bar(dr), 0);
+      }
+      __syncwarp();
     }
-    if (*abort) {  // let issued MMAs finish before TMEM is freed
-      const int dr = is_s ? kBarDrainS : kBarDrain;
-      mma_commit_e(bar(dr));
-      if (lane == 0) drain_wait(bar(dr), 0);
-    }
-    __syncwarp();
   } else {
     // --------------------------------------------- softmax warpgroups
+    regs_inc<216>();
     const int wg = warp >> 2;
     const int r = tid & 127;  // tile row = TMEM lane
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    volatile uint32_t *xflags = reinterpret_cast<volatile uint32_t *>(smem_raw + L::kFlags);
-    float *xsum = reinterpret_cast<float *>(smem_raw + L::kXsum);
+    const uint32_t tS = tS0 + uint32_t(wg) * 128u + lane_off, tO = tO0 + uint32_t(wg * D) + lane_off;
+    float2 *s_ml = reinterpret_cast<float2 *>(smem_raw + L::kMl);
     uint32_t x_it = 0, seg_n = 0;
     auto rendezvous = [&]() {  // the warps that hold the same 32 rows (bounded)
       mbar_arrive(bar(kBarXchg + (warp & 3)));
@@ -318,31 +370,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++x_it;
       return ok;
     };
-    while (ok && cursor_next(p, st, cursor, d, seg, here)) {
-      const DecRows v = dec_rows(p, d, seg.tile);
-      const int64_t qb = p.cu_q ? 0 : here.b;
-      const int kvlen = d.kv.kvlen, qbase = kvlen - d.q.qlen;
-      const int xr = v.first + min(r, v.rows - 1);
-      const int tq = v.t0 + xr / p.gg;
-      // ---- the Q tile, once the segment before has read its own
-      if (!(ok = wait_warp(bar(kBarQEmpty), (seg_n & 1u) ^ 1u, abort, status))) break;
-      {
-        constexpr int kPieces = D / 8;  // 16-byte pieces of a row
-        for (int i = tid; i < kTile * kPieces; i += kSoftmaxThreads) {
-          const int rr = i / kPieces, c = i % kPieces;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (rr < v.rows) {
-            const int y = v.first + rr, t = v.t0 + y / p.gg, h = seg.hh * p.gg + y % p.gg;
-            const T *q = static_cast<const T *>(p.q) + qb * p.q_sb + (d.q.tok0 + t) * p.q_st + int64_t(h) * p.q_sh;
-            x = __ldg(reinterpret_cast<const uint4 *>(q) + c);
-          }
-          // 128-byte swizzle: the 16-byte piece within a row of 128 bytes xor the row
-          *reinterpret_cast<uint4 *>(smem_raw + L::kQ + (c >> 3) * L::kBox + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kBarQFull));
+    // Q of a segment into shared memory, once the segment before has read its
+    // own; all loads of a thread in flight together
+    auto gather_q = [&](const volatile SegInfo &g) {
+      const int first = g.first, rows = g.rows, t0 = g.t0, h0 = g.hh * p.gg;
+      const T *q = static_cast<const T *>(p.q) + g.b * p.q_sb + (int64_t(g.tok0) + t0) * p.q_st;
+      constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+      constexpr int kRounds = kTile * kPieces / kSoftmaxThreads;
+      const int c = tid % kPieces;
+      uint4 x[kRounds];
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int rr = tid / kPieces + i * (kSoftmaxThreads / kPieces), y = first + rr;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (rr < rows)
+          x[i] = __ldg(reinterpret_cast<const uint4 *>(q + int64_t(y / p.gg) * p.q_st + int64_t(h0 + y % p.gg) * p.q_sh) + c);
       }
-      const int64_t *bits = p.tree ? p.tree + qb * p.t_sb + (d.q.tok0 + tq) * p.t_st : nullptr;
+      if (!(ok = wait_warp(bar(kBarQEmpty), (seg_n & 1u) ^ 1u, abort, status))) return;
+      ++seg_n;
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int rr = tid / kPieces + i * (kSoftmaxThreads / kPieces);
+        // 128-byte swizzle: the 16-byte piece within a row of 128 bytes xor the row
+        *reinterpret_cast<uint4 *>(smem_raw + L::kQ + (c >> 3) * L::kBox + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kBarQFull));
+    };
+    const volatile ChunkList *list = next_segment();
+    if (list) gather_q(list->seg);
+    while (ok && list) {
+      const volatile SegInfo &g = list->seg;  // read before the list is given back
+      const int kvlen = g.kvlen, qbase = kvlen - g.qlen, qb = g.b, slot = g.slot;
+      const bool live = r < g.rows;
+      const int xr = g.first + min(r, g.rows - 1);
+      const int tq = g.t0 + xr / p.gg, row = g.tok0 + tq, head = g.hh * p.gg + xr % p.gg;
+      const int64_t *bits = p.tree ? p.tree + qb * p.t_sb + int64_t(row) * p.t_st : nullptr;
       // the columns [u, u + 64) that the row sees
       auto visible = [&](int u) {
         uint64_t m = low_bits(int64_t(kvlen) - u);
@@ -352,157 +415,144 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const int edge_from = (p.tree || p.causal) ? qbase : kvlen;  // first token that some row may not see
       float m = -INFINITY, l = 0.f;
-      int n = 0;
+      int n = 0;  // chunks of this group
       each_chunk([&](const int u0c, int) {
-        const int b = int(kv_it % kSBufs);
-        if (!(ok = wait_warp(bar(kBarSFull + b), (kv_it / kSBufs) & 1u, abort, status))) return;
+        const uint32_t t = kv_it++;
+        if (int(t & 1u) != wg) return;
+        if (!(ok = wait_warp(bar(kBarSFull + wg), (t / 2) & 1u, abort, status))) return;
         tc_fence_after();
-        const uint32_t tS = tS0 + uint32_t(b) * 128u + lane_off;
         const int valid_all = kvlen - u0c;
         if (valid_all < 128) {
           // rows past the used length may hold anything: their weights are 0,
           // and their V is made 0 as well before P is published
-          const int sg = int(kv_it % kStages);
-          if (!(ok = wait_warp(bar(kBarVFull + sg), (kv_it / kStages) & 1u, abort, status))) return;
+          const int sg = int(t % kStages);
+          if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
           uint4 *vt = reinterpret_cast<uint4 *>(smem_raw + L::kV + sg * L::kTileBytes);
           const int per_half = (128 - valid_all) * 8;
-          for (int w = tid; w < per_half * (D / 64); w += kSoftmaxThreads) {
+          for (int w = r; w < per_half * (D / 64); w += 128) {
             const int h = w / per_half, x = w % per_half;
             vt[h * (L::kBox / 16) + valid_all * 8 + x] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
-        const bool edge = u0c + kChunk > edge_from;
-        uint32_t x[kCols];
-        tmem_ld_cols<kCols>(tS + uint32_t(kCols * wg), x);
+        uint32_t x[128];
+        tmem_ld_cols<128>(tS, x);
         tmem_wait_ld();
-        if (edge) {
-          const uint64_t vis = visible(u0c + kCols * wg);
-          const uint32_t lo = uint32_t(vis), hi = uint32_t(vis >> 32);
+        if (u0c + kChunk > edge_from) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (!((c < 32 ? lo : hi) & (1u << (c & 31)))) x[c] = __float_as_uint(-INFINITY);
-        }
-        float ps[2] = {0.f, 0.f};
-        uint32_t pk[kCols / 2];
-        auto exps = [&](float mm) {
-          ps[0] = ps[1] = 0.f;
-#pragma unroll
-          for (int c = 0; c < kCols; c += 2) {
-            const float e0 = ex2(fmaf(__uint_as_float(x[c]), p.scale_log2, -mm));
-            const float e1 = ex2(fmaf(__uint_as_float(x[c + 1]), p.scale_log2, -mm));
-            ps[(c >> 1) & 1] += e0 + e1;
-            pk[c >> 1] = Pack2<T>::pack(e0, e1);
-          }
-        };
-        // a row that has seen nothing yet keeps m = -inf and asks for a reference
-        const bool first = m == -INFINITY;
-        if (!first) exps(m);
-        uint32_t any = 1;
-        if (n > 0) {
-          const uint32_t need = __any_sync(0xffffffffu, first || !(ps[0] + ps[1] <= kRescaleSum)) ? 1u : 0u;
-          if (lane == 0) xflags[(kv_it & 1u) * 8 + warp] = need;
-          if (!rendezvous()) return;
-          any = xflags[(kv_it & 1u) * 8 + (warp & 3)] | xflags[(kv_it & 1u) * 8 + 4 + (warp & 3)];
-        }
-        float alpha = 1.f;
-        const bool grow = any != 0u;
-        if (grow) {
-          float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) pm[c & 3] = fmaxf(pm[c & 3], __uint_as_float(x[c]));
-          float cm = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-          // the other group's columns are still S in TMEM
-          const uint64_t vo = edge ? visible(u0c + kCols * (wg ^ 1)) : ~0ull;
-#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            uint32_t y[kCols / 2];
-            tmem_ld_cols<kCols / 2>(tS + uint32_t(kCols * (wg ^ 1) + (kCols / 2) * h), y);
-            tmem_wait_ld();
-            const uint32_t vy = uint32_t(vo >> (32 * h));
+            const uint64_t vis = visible(u0c + 64 * h);
+            const uint32_t lo = uint32_t(vis), hi = uint32_t(vis >> 32);
 #pragma unroll
-            for (int c = 0; c < kCols / 2; ++c)
-              if (vy & (1u << c)) cm = fmaxf(cm, __uint_as_float(y[c]));
+            for (int c = 0; c < 64; ++c)
+              if (!((c < 32 ? lo : hi) & (1u << (c & 31)))) x[64 * h + c] = __float_as_uint(-INFINITY);
           }
-          if (!rendezvous()) return;  // nobody overwrites S with P before every thread has read it
-          const float m_new = fmaxf(m, cm * p.scale_log2);
-          alpha = first ? 1.f : ex2(m - m_new);
-          m = m_new;
-          exps(m > -INFINITY ? m : 0.f);  // nothing visible yet: every weight is 0
         }
-        tmem_st_cols<kCols / 2>(tS + uint32_t(kCols * wg), pk);
-        l = l * alpha + (ps[0] + ps[1]);
-        if (grow && n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O may be rescaled once every earlier product has landed
-          const uint32_t t = kv_it - 1;
-          if (!(ok = wait_warp(bar(kBarPVDone + int(t & 1u)), (t / 2) & 1u, abort, status))) return;
-          tc_fence_after();
-          const uint32_t col = tO + lane_off + uint32_t(wg * (D / 2));
-          uint32_t o[D / 2];
-          tmem_ld_cols<D / 2>(col, o);
-          tmem_wait_ld();
+        float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < D / 2; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-          tmem_st_cols<D / 2>(col, o);
+        for (int c = 0; c < 128; ++c) pm[c & 3] = fmaxf(pm[c & 3], __uint_as_float(x[c]));
+        const float cm = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * p.scale_log2;
+        const bool move = cm > m + kSlack;  // (true for a first finite maximum)
+        if (__any_sync(0xffffffffu, move)) {
+          const float m_new = move ? cm : m;
+          const float alpha = move ? ex2(m - m_new) : 1.f;
+          m = m_new;
+          l *= alpha;
+          if (n > 0) {  // the product before is in O: this S waited for it
+#pragma unroll
+            for (int h = 0; h < D / 32; ++h) {
+              uint32_t o[32];
+              tmem_ld32(tO + uint32_t(32 * h), o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tmem_st32(tO + uint32_t(32 * h), o);
+            }
+          }
         }
+        const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: every weight is 0
+        float2 ps[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        const float2 sc = {p.scale_log2, p.scale_log2}, mm = {-ref, -ref};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float2 a = fma2(make_float2(__uint_as_float(x[64 * h + c]), __uint_as_float(x[64 * h + c + 1])), sc, mm);
+            const float2 e = {ex2(a.x), ex2(a.y)};
+            ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], e);
+            pk[c >> 1] = Pack2<T>::pack(e.x, e.y);
+          }
+          tmem_st32(tS + uint32_t(32 * h), pk);  // the whole row of S is in registers
+        }
+        l += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(kBarPFull + b));
+        mbar_arrive(bar(kBarPFull + wg));
         ++n;
-        ++kv_it;
       });
       if (!ok) break;
-      // ---- epilogue: the finished rows, or this block's part of them
+      // the next segment's Q first: its first scores are computed meanwhile
+      list = next_segment();
+      if (list) gather_q(list->seg);
+      if (!ok) break;
+      // ---- epilogue: the finished rows, or this block's part of them; group
+      // w writes half of the columns from both groups' outputs
       if (n > 0) {
-        const uint32_t t = kv_it - 1;
-        if (!(ok = wait_warp(bar(kBarPVDone + int(t & 1u)), (t / 2) & 1u, abort, status))) break;
-        tc_fence_after();
+        const uint32_t t = kv_it - 1 - uint32_t(int((kv_it - 1) & 1u) != wg);  // this group's last chunk
+        if (!(ok = wait_warp(bar(kBarPVDone + wg), (t / 2) & 1u, abort, status))) break;
       }
-      // the partner has read the last segment's sums: it has met this warp
-      // since, in the first chunk or here
-      if (n == 0 && !rendezvous()) break;
-      xsum[wg * 128 + r] = l;
+      s_ml[wg * 128 + r] = make_float2(m, l);
       if (!rendezvous()) break;
-      const float lsum = xsum[r] + xsum[128 + r];
-      const bool whole = seg.cs == 0 && seg.ce == d.chunks;
-      const int slot = here.pos == st.lo ? 2 * int(blockIdx.x) : 2 * int(blockIdx.x) + 1;
-      uint32_t o[D / 2];
-      if (n > 0) {
-        tmem_ld_cols<D / 2>(tO + lane_off + uint32_t(wg * (D / 2)), o);
-        tmem_wait_ld();
-      } else {
+      tc_fence_after();
+      const float2 other = s_ml[(wg ^ 1) * 128 + r];
+      const float mx = fmaxf(m, other.x), mref = mx == -INFINITY ? 0.f : mx;
+      const float f_own = ex2(m - mref), f_other = ex2(other.x - mref);
+      const float lsum = l * f_own + other.y * f_other;
+      // a group that saw nothing may have no output at all: its columns are not used
+      const float f0 = wg ? f_other : f_own, f1 = wg ? f_own : f_other;
+      const bool s0 = (wg ? other.x : m) != -INFINITY, s1 = (wg ? m : other.x) != -INFINITY;
+      float o[D / 2];
 #pragma unroll
-        for (int c = 0; c < D / 2; ++c) o[c] = 0u;
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t a[32], b[32];
+        const uint32_t col = uint32_t(wg * (D / 2) + 32 * h) + lane_off;
+        tmem_ld32(tO0 + col, a);
+        tmem_ld32(tO0 + uint32_t(D) + col, b);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          o[32 * h + c] = (s0 ? __uint_as_float(a[c]) * f0 : 0.f) + (s1 ? __uint_as_float(b[c]) * f1 : 0.f);
       }
-      if (r < v.rows) {
-        const int h = seg.hh * p.gg + xr % p.gg;
-        if (whole) {
-          const float inv = lsum > 0.f || lsum != lsum ? 1.f / lsum : 0.f;
-          T *dst = static_cast<T *>(p.out) + qb * p.o_sb + (d.q.tok0 + tq) * p.o_st + int64_t(h) * p.o_sh + wg * (D / 2);
+      tc_fence_before();
+      // the next segment's products write both outputs, and the states' memory is used again
+      if (!rendezvous()) break;
+      if (live) {
+        if (slot < 0) {
+          const bool some = lsum > 0.f || lsum != lsum;
+          const float inv = some ? 1.f / lsum : 0.f;
+          T *dst = static_cast<T *>(p.out) + qb * p.o_sb + int64_t(row) * p.o_st + int64_t(head) * p.o_sh + wg * (D / 2);
 #pragma unroll
           for (int c8 = 0; c8 < D / 16; ++c8) {
             uint4 w;
-            w.x = Pack2<T>::pack(__uint_as_float(o[8 * c8]) * inv, __uint_as_float(o[8 * c8 + 1]) * inv);
-            w.y = Pack2<T>::pack(__uint_as_float(o[8 * c8 + 2]) * inv, __uint_as_float(o[8 * c8 + 3]) * inv);
-            w.z = Pack2<T>::pack(__uint_as_float(o[8 * c8 + 4]) * inv, __uint_as_float(o[8 * c8 + 5]) * inv);
-            w.w = Pack2<T>::pack(__uint_as_float(o[8 * c8 + 6]) * inv, __uint_as_float(o[8 * c8 + 7]) * inv);
+            w.x = Pack2<T>::pack(o[8 * c8] * inv, o[8 * c8 + 1] * inv);
+            w.y = Pack2<T>::pack(o[8 * c8 + 2] * inv, o[8 * c8 + 3] * inv);
+            w.z = Pack2<T>::pack(o[8 * c8 + 4] * inv, o[8 * c8 + 5] * inv);
+            w.w = Pack2<T>::pack(o[8 * c8 + 6] * inv, o[8 * c8 + 7] * inv);
             reinterpret_cast<uint4 *>(dst)[c8] = w;
           }
           if (wg == 0 && p.lse)
-            p.lse[qb * p.l_sb + (d.q.tok0 + tq) * p.l_st + int64_t(h) * p.l_sh] =
-                lsum > 0.f || lsum != lsum ? (m + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+            p.lse[qb * p.l_sb + int64_t(row) * p.l_st + int64_t(head) * p.l_sh] =
+                some ? (mx + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
         } else {
-          float4 *dst = reinterpret_cast<float4 *>(p.part_o + (int64_t(slot) * kTile + r) * D + wg * (D / 2));
+          // four columns of all rows side by side: a warp's stores are contiguous
+          float4 *dst = reinterpret_cast<float4 *>(p.part_o) + (int64_t(slot) * (D / 4) + wg * (D / 8)) * kTile + r;
 #pragma unroll
           for (int c4 = 0; c4 < D / 8; ++c4)
-            dst[c4] = make_float4(__uint_as_float(o[4 * c4]), __uint_as_float(o[4 * c4 + 1]),
-                                  __uint_as_float(o[4 * c4 + 2]), __uint_as_float(o[4 * c4 + 3]));
-          if (wg == 0) reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * kTile + r] = make_float2(m, lsum);
+            dst[c4 * kTile] = make_float4(o[4 * c4], o[4 * c4 + 1], o[4 * c4 + 2], o[4 * c4 + 3]);
+          if (wg == 0) reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * kTile + r] = make_float2(mx, lsum);
         }
       }
-      if (tid == 0 && seg.cs == 0 && !whole) p.join[blockIdx.x] = dec_join(p, st, here, d, seg, v, slot);
-      tc_fence_before();
-      ++seg_n;
     }
   }
   tc_fence_before();
