@@ -64,6 +64,9 @@ struct DecodeProblem {
   int32_t TR;         // query rows of a tile
   int32_t chunk;      // kv tokens of a work unit's step
   int32_t grid;       // blocks of the attention kernel
+  int32_t tr_sh, chunk_sh, bq_sh, bkv_sh;  // base-2 logarithms
+  int32_t tpb;        // tiles of a query block (sparse)
+  uint32_t gg_inv;    // ceil(2^32 / gg), 0 for 1
   int32_t group;      // blocks that take the same chunks for different row tiles
   int32_t tree_words;
   int64_t Sq, Tq;
@@ -92,8 +95,9 @@ cudaError_t launch_select_blocks(const SelectProblem &p, cudaStream_t s);
 cudaError_t launch_decode(const DecodeProblem &p, cudaStream_t s);
 cudaError_t launch_decode_tc(const DecodeProblem &p, cudaStream_t s);
 void decode_tc_plan(DecodeProblem &p);
-// fills the tile, step and grid of a problem whose sizes are set
-void decode_plan(DecodeProblem &p);
+// fills the tile, step and grid of a problem whose sizes are set; false: too
+// large for one call
+bool decode_plan(DecodeProblem &p);
 
 #ifdef __CUDACC__
 struct KvBatch {

@@ -328,7 +328,7 @@ bsa_status prepare_decode(const bsa_tensor *q, const bsa_tensor *k, const bsa_te
   p.k = k->data; kv_strides(k, P.kv_layout, p.k_sb, p.k_sh, p.k_st);
   p.v = v->data; kv_strides(v, P.kv_layout, p.v_sb, p.v_sh, p.v_st);
   p.out = out->data; q_strides(out, P.q_layout, p.o_sb, p.o_sh, p.o_st);
-  if (!empty) decode_plan(p);
+  if (!empty && !decode_plan(p)) return BSA_ERR_UNSUPPORTED;
   uint64_t cur = 0;
   place(cur, kStWords * 4, L.status);
   place(cur, uint64_t(p.grid) * 4, L.flags);

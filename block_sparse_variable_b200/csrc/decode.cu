@@ -35,8 +35,8 @@ struct Smem {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kRing = kStages * kStage;          // of one warp
   static constexpr int kMl = kWarps * kRing;              // [warps][rows][2] floats
-  static constexpr int kBlk = kMl + kWarps * kTile * 8;   // [warps][32] ints
-  static constexpr int kU = kBlk + kWarps * 128;          // [warps][stages] first token of a stage
+  static constexpr int kBlk = kMl + kWarps * kTile * 8;   // [warps][32] ids
+  static constexpr int kU = kBlk + kWarps * 64;           // [warps][stages] first token of a stage
   static constexpr int kBytes = kU + kWarps * kStages * 4;
   static_assert(kWarps * kTile * D * 4 <= kWarps * kRing, "the states are joined in the ring's memory");
 };
@@ -79,7 +79,7 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
 template <typename T>
 __device__ __forceinline__ void write_row(const DecodeProblem &p, int64_t tok0, int b, int hh, int t0, int x, int c,
                                           float4 o, float m, float l) {
-  const int t = t0 + x / p.gg, h = hh * p.gg + x % p.gg;
+  const int y = div_gg(p, x), t = t0 + y, h = hh * p.gg + x - y * p.gg;
   const bool some = l > 0.f || l != l;
   const float inv = some ? 1.f / l : 0.f;
   uint2 w;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
   const uint32_t ring = smem_u32(smem) + uint32_t(warp * S::kRing);
   float *s_o = reinterpret_cast<float *>(smem);
   float2 *s_ml = reinterpret_cast<float2 *>(smem + S::kMl);
-  int *s_blk = reinterpret_cast<int *>(smem + S::kBlk) + warp * 32;
+  uint16_t *s_blk = reinterpret_cast<uint16_t *>(smem + S::kBlk) + warp * 32;
   int *s_u = reinterpret_cast<int *>(smem + S::kU) + warp * kStages;
   DecodeJoin join{};
 
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 4) k_decode(const Dec
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r = (lane >> 2) + 8 * half, x = v.first + min(r, v.rows - 1);
-      const int t = v.t0 + x / p.gg, h = hh * p.gg + x % p.gg;
+      const int y = div_gg(p, x), t = v.t0 + y, h = hh * p.gg + x - y * p.gg;
       const int64_t qb = p.cu_q ? 0 : b;
       const T *q = static_cast<const T *>(p.q) + qb * p.q_sb + (d.q.tok0 + t) * p.q_st + int64_t(h) * p.q_sh;
 #pragma unroll
@@ -496,13 +496,30 @@ cudaError_t launch_mask(const DecodeProblem &p, cudaStream_t s) {
 
 }  // namespace
 
-void decode_plan(DecodeProblem &p) {
-  const int64_t tokens = p.q_layout == BSA_LAYOUT_BNSD ? p.Sq : (p.Tq + p.B - 1) / p.B;
-  if (tokens * p.gg > kFewRows) return decode_tc_plan(p);
-  p.TR = kTile;
-  p.chunk = kChunk;
-  p.group = 1;
-  p.grid = num_sms() * (p.D == 128 ? 2 : 4);
+bool decode_plan(DecodeProblem &p) {
+  const int64_t tokens = p.q_layout == BSA_LAYOUT_BNSD ? p.Sq : (p.Tq + p.B - 1) / p.B;  // the mean
+  const bool few = tokens * p.gg <= kFewRows;
+  if (few) {
+    p.TR = kTile;
+    p.chunk = kChunk;
+    p.group = 1;
+    p.grid = num_sms() * (p.D == 128 ? 2 : 4);
+  } else {
+    decode_tc_plan(p);
+  }
+  auto log2 = [](int64_t x) { int n = 0; while ((int64_t(1) << n) < x) ++n; return n; };
+  p.tr_sh = log2(p.TR);
+  p.chunk_sh = log2(p.chunk);
+  p.bq_sh = log2(p.BQ);
+  p.bkv_sh = log2(p.kv.BKV);
+  p.tpb = int32_t((int64_t(p.BQ) * p.gg + p.TR - 1) >> p.tr_sh);
+  p.gg_inv = p.gg == 1 ? 0u : uint32_t(((int64_t(1) << 32) + p.gg - 1) / p.gg);
+  // chunks of all units, at most
+  const int64_t all = p.q_layout == BSA_LAYOUT_BNSD ? p.Sq * p.B : p.Tq;
+  const int64_t tiles = ((all * p.gg) >> p.tr_sh) + (p.index ? (all >> p.bq_sh) + p.B : p.B) + int64_t(p.group) * p.B;
+  const int64_t kv = p.kv.layout == BSA_LAYOUT_TND ? p.kv.Tkv : p.kv.Skv;
+  const int64_t chunks = ((kv + p.chunk - 1) >> p.chunk_sh) + 1;
+  return p.gg < 65536 - 256 && double(tiles) * double(p.H) * double(chunks) < 4.0e9;
 }
 
 cudaError_t launch_decode(const DecodeProblem &p, cudaStream_t s) {

@@ -25,48 +25,50 @@
 namespace bsa {
 namespace {
 
+// Positions on the line are unsigned 32-bit numbers (the host refuses sizes
+// that could pass them): a 64-bit division takes some 500 clocks, and several
+// stand between a launch and its first load.
 struct DecBatch {
   QBatch q;
   KvBatch kv;
-  int nk;       // kv blocks (sparse)
-  int tiles;    // row tiles per head
-  int passes;   // turns of a group of blocks over them
-  int chunks;   // chunks of a unit
-  int64_t work; // chunks of all units of the batch
+  int nk;         // kv blocks (sparse)
+  int tiles;      // row tiles per head
+  int passes;     // turns of a group of blocks over them
+  int chunks;     // chunks of a unit
+  uint32_t work;  // chunks of all units of the batch
 };
 
 __device__ __forceinline__ DecBatch dec_batch(const DecodeProblem &p, int b, uint32_t &flags) {
   DecBatch d;
   d.q = q_batch(p.cu_q, p.Sq, p.Tq, b, flags);
   d.kv = kv_batch(p.kv, b, flags);
-  d.nk = (d.kv.kvlen + p.kv.BKV - 1) / p.kv.BKV;
-  const int64_t gg = p.gg;
-  int64_t tiles;
+  d.nk = (d.kv.kvlen + p.kv.BKV - 1) >> p.bkv_sh;
+  const int up = p.TR - 1;
   if (p.index) {  // a tile's rows share an index row: tiles do not cross query blocks
-    const int full = d.q.qlen / p.BQ, rem = d.q.qlen % p.BQ;
-    tiles = int64_t(full) * ((p.BQ * gg + p.TR - 1) / p.TR) + (rem * gg + p.TR - 1) / p.TR;
-    d.chunks = max(1, min(p.W, d.nk) * (p.kv.BKV / p.chunk));
+    const int full = d.q.qlen >> p.bq_sh, rem = d.q.qlen & (p.BQ - 1);
+    d.tiles = full * p.tpb + ((rem * p.gg + up) >> p.tr_sh);
+    d.chunks = max(1, min(p.W, d.nk) << (p.bkv_sh - p.chunk_sh));
   } else {
-    tiles = (d.q.qlen * gg + p.TR - 1) / p.TR;
-    d.chunks = max(1, (d.kv.kvlen + p.chunk - 1) / p.chunk);
+    d.tiles = (d.q.qlen * p.gg + up) >> p.tr_sh;
+    d.chunks = max(1, (d.kv.kvlen + p.chunk - 1) >> p.chunk_sh);
   }
-  d.tiles = int(tiles);
-  d.passes = (d.tiles + p.group - 1) / p.group;
-  d.work = int64_t(d.passes) * p.H * d.chunks;
+  d.passes = p.group == 1 ? d.tiles : int(unsigned(d.tiles + p.group - 1) / unsigned(p.group));
+  d.work = uint32_t(d.passes) * uint32_t(p.H) * uint32_t(d.chunks);
   return d;
 }
 
 // where a block of the grid begins and how far it goes
 struct DecStart {
-  int64_t total, lo, hi;  // chunks of the call; this group's range
-  int64_t rem;            // first chunk within batch b
-  int64_t groups;         // groups of blocks that have work
+  uint32_t lo, hi;        // this group's range
+  uint32_t rem;           // first chunk within batch b
+  uint32_t each, extra;   // chunks of a group; the first `extra` groups have one more
   int b, qoff;            // batch of the first chunk; index rows of the batches before it
 };
 
 template <int kThreads>
 struct DecScratch {
-  int64_t work[kThreads / 32], rows[kThreads / 32];
+  uint32_t work[kThreads / 32];
+  int rows[kThreads / 32];
   DecStart start;
 };
 
@@ -76,54 +78,68 @@ __device__ DecStart dec_start(const DecodeProblem &p, DecScratch<kThreads> &sh, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int64_t work = 0, rows = 0;
+  uint32_t work = 0;
+  int rows = 0;
   for (int b = b0; b < b1; ++b) {
     const DecBatch d = dec_batch(p, b, flags);
     work += d.work;
-    rows += (d.q.qlen + p.BQ - 1) / p.BQ;
+    rows += (d.q.qlen + p.BQ - 1) >> p.bq_sh;
   }
-  int64_t iw = work, ir = rows;
+  uint32_t iw = work;
+  int ir = rows;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, iw, o), y = __shfl_up_sync(0xffffffffu, ir, o);
+    const uint32_t x = __shfl_up_sync(0xffffffffu, iw, o);
+    const int y = __shfl_up_sync(0xffffffffu, ir, o);
     if (lane >= o) iw += x, ir += y;
   }
   if (lane == 31) sh.work[warp] = iw, sh.rows[warp] = ir;
   __syncthreads();
-  int64_t total = 0, bw = iw - work, br = ir - rows;
+  uint32_t total = 0, bw = iw - work;
+  int br = ir - rows;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) bw += sh.work[w], br += sh.rows[w];
     total += sh.work[w];
   }
-  const int64_t groups = gridDim.x / unsigned(p.group);
-  const int64_t G = groups < total ? groups : total;
-  const int64_t c = blockIdx.x / unsigned(p.group);
-  if (c < G) {
-    const int64_t lo = c * total / G;
-    if (lo >= bw && lo < bw + work) {
+  const uint32_t groups = gridDim.x / unsigned(p.group), c = blockIdx.x / unsigned(p.group);
+  const uint32_t each = total / groups, extra = total % groups;
+  const uint32_t lo = c * each + min(c, extra), hi = lo + each + (c < extra ? 1u : 0u);
+  if (lo < hi) {
+    if (lo >= bw && lo - bw < work) {
       uint32_t ignore = 0;
       for (int b = b0; b < b1; ++b) {
         const DecBatch d = dec_batch(p, b, ignore);
-        if (lo < bw + d.work) {
-          sh.start = {total, lo, (c + 1) * total / G, lo - bw, G, b, int(br)};
+        if (lo - bw < d.work) {
+          sh.start = {lo, hi, lo - bw, each, extra, b, br};
           break;
         }
         bw += d.work;
-        br += (d.q.qlen + p.BQ - 1) / p.BQ;
+        br += (d.q.qlen + p.BQ - 1) >> p.bq_sh;
       }
     }
   } else if (tid == 0) {
-    sh.start = {total, total, total, 0, G, 0, 0};
+    sh.start = {lo, lo, 0, each, extra, p.B, 0};
   }
   __syncthreads();
   return sh.start;
+}
+
+// the group that owns chunk x of the line
+__device__ __forceinline__ uint32_t dec_owner(const DecStart &s, uint32_t x) {
+  const uint32_t big = s.extra * (s.each + 1);  // each >= 1 past it
+  return x < big ? x / (s.each + 1) : s.extra + (x - big) / s.each;
 }
 
 // a block's share of one unit
 struct DecSeg {
   int hh, tile, cs, ce;  // head group, row tile, chunks [cs, ce)
 };
+
+// y / gg for y < 2^16: the rows of a tile
+__device__ __forceinline__ int div_gg(const DecodeProblem &p, int y) {
+  return p.gg == 1 ? y : int(__umulhi(unsigned(y), p.gg_inv));
+}
 
 // the query rows of a tile
 struct DecRows {
@@ -133,16 +149,19 @@ struct DecRows {
 __device__ __forceinline__ DecRows dec_rows(const DecodeProblem &p, const DecBatch &d, int tile) {
   DecRows v;
   if (p.index) {
-    const int tpb = int((int64_t(p.BQ) * p.gg + p.TR - 1) / p.TR);
-    v.irow = tile / tpb;
-    v.t0 = v.irow * p.BQ;
-    v.first = (tile % tpb) * p.TR;
-    v.rows = min(p.TR, min(p.BQ, d.q.qlen - v.t0) * p.gg - v.first);
+    v.irow = tile / p.tpb;
+    v.t0 = v.irow << p.bq_sh;
+    int first = (tile - v.irow * p.tpb) << p.tr_sh;
+    v.rows = min(p.TR, min(p.BQ, d.q.qlen - v.t0) * p.gg - first);
+    const int t = first / p.gg;
+    v.t0 += t;
+    v.first = first - t * p.gg;
   } else {
+    const int x = tile << p.tr_sh;
     v.irow = 0;
-    v.t0 = int(int64_t(tile) * p.TR / p.gg);
-    v.first = int(int64_t(tile) * p.TR % p.gg);
-    v.rows = int(min(int64_t(p.TR), int64_t(d.q.qlen) * p.gg - int64_t(tile) * p.TR));
+    v.t0 = x / p.gg;
+    v.first = x - v.t0 * p.gg;
+    v.rows = min(p.TR, d.q.qlen * p.gg - x);
   }
   return v;
 }
@@ -172,7 +191,7 @@ __device__ __forceinline__ DecWalk walk_begin(const DecodeProblem &p, int b, int
 // accept entries up to number `until`, by a converged warp; entry number
 // first + i goes to blk[i] (shared memory of the warp)
 __device__ __forceinline__ void walk_accept(const DecodeProblem &p, int nk, DecWalk &w, int first, int until,
-                                            int *blk, int lane) {
+                                            uint16_t *blk, int lane) {
   while (w.taken < until && w.slot < p.W) {
     const int s = w.slot + lane;
     const int e = s < p.W ? int(w.row[s]) : int(kNoBlock);
@@ -193,7 +212,7 @@ __device__ __forceinline__ void walk_accept(const DecodeProblem &p, int nk, DecW
     const uint32_t kept = __ballot_sync(0xffffffffu, keep);
     const int n = __popc(kept);
     const int end = n == room ? 32 - __clz(kept) : 32;  // slots consumed
-    if (keep && w.taken + rank >= first) blk[w.taken + rank - first] = e;
+    if (keep && w.taken + rank >= first) blk[w.taken + rank - first] = uint16_t(e);
     if (__any_sync(0xffffffffu, lane < end && used && !take)) w.flags |= BSA_FLAG_BAD_INDEX;
     w.last = max(w.last, __shfl_sync(0xffffffffu, pre, end - 1));
     w.taken += n;
@@ -203,22 +222,23 @@ __device__ __forceinline__ void walk_accept(const DecodeProblem &p, int nk, DecW
 }
 
 // Chunks [x, x + 32) of the unit, one a lane; x is a multiple of 32, so that
-// no entry is divided between two fetches.  blk: 32 words of the warp.
+// no entry is divided between two fetches.  blk: 32 ids in the warp's shared
+// memory.
 __device__ __forceinline__ void walk_fetch(const DecodeProblem &p, const DecBatch &d, int b, DecWalk &w, int x,
-                                           int ce, int *blk, int lane, int &u, int &page) {
+                                           int ce, uint16_t *blk, int lane, int &u, int &page) {
   u = -1;
   page = 0;
   if (p.index) {
-    const int cpb = p.kv.BKV / p.chunk;  // 1 .. 16
-    const int first = x / cpb;
+    const int cpb_sh = p.bkv_sh - p.chunk_sh;  // 1 .. 16 chunks a block
+    const int first = x >> cpb_sh;
     // the unit's last fetch reads the rest of the row, for its bad entries
-    const int until = x + 32 >= d.chunks ? INT_MAX : (x + 32) / cpb;
+    const int until = x + 32 >= d.chunks ? INT_MAX : (x + 32) >> cpb_sh;
     walk_accept(p, d.nk, w, first, until, blk, lane);
-    const int e = (x + lane) / cpb;
-    if (x + lane < ce && e < w.taken) u = blk[e - first] * p.kv.BKV + (x + lane) % cpb * p.chunk;
+    const int e = (x + lane) >> cpb_sh;
+    if (x + lane < ce && e < w.taken) u = (int(blk[e - first]) << p.bkv_sh) + (((x + lane) & ((1 << cpb_sh) - 1)) << p.chunk_sh);
     __syncwarp();
   } else if (x + lane < ce) {
-    u = (x + lane) * p.chunk;
+    u = (x + lane) << p.chunk_sh;
   }
   if (u >= d.kv.kvlen) u = -1;
   if (u >= 0) {
@@ -229,30 +249,31 @@ __device__ __forceinline__ void walk_fetch(const DecodeProblem &p, const DecBatc
 
 // A block's place on the line: the segment it is at.
 struct DecCursor {
-  int64_t pos, rem;  // chunk of the line, chunk within the batch
+  uint32_t pos, rem;  // chunk of the line, chunk within the batch
   int b, qoff;
 };
 __device__ __forceinline__ DecCursor cursor_begin(const DecStart &s) { return {s.lo, s.rem, s.b, s.qoff}; }
 // the segment at the cursor, which is then moved past it; false at the end
 __device__ __forceinline__ bool cursor_next(const DecodeProblem &p, const DecStart &s, DecCursor &c, DecBatch &d,
                                             DecSeg &g, DecCursor &at) {
-  while (c.pos < s.hi) {
+  while (c.pos < s.hi && c.b < p.B) {  // (contradictory lengths can end the batches first)
     uint32_t ignore = 0;
     d = dec_batch(p, c.b, ignore);
     if (c.rem >= d.work) {
       c.rem -= d.work;
-      c.qoff += (d.q.qlen + p.BQ - 1) / p.BQ;
+      c.qoff += (d.q.qlen + p.BQ - 1) >> p.bq_sh;
       ++c.b;
       continue;
     }
-    const int64_t unit = c.rem / d.chunks;
-    g.cs = int(c.rem % d.chunks);
-    g.ce = int(min(int64_t(d.chunks), g.cs + (s.hi - c.pos)));
-    g.hh = int(unit / d.passes);
-    g.tile = int(unit % d.passes) * p.group + int(blockIdx.x) % p.group;
+    const uint32_t unit = c.rem / uint32_t(d.chunks);
+    g.cs = int(c.rem - unit * uint32_t(d.chunks));
+    g.ce = int(min(uint32_t(d.chunks), uint32_t(g.cs) + (s.hi - c.pos)));
+    g.hh = int(unit / uint32_t(d.passes));
+    g.tile = int(unit - uint32_t(g.hh) * uint32_t(d.passes));
+    if (p.group > 1) g.tile = g.tile * p.group + int(blockIdx.x % unsigned(p.group));
     at = c;
-    c.pos += g.ce - g.cs;
-    c.rem += g.ce - g.cs;
+    c.pos += uint32_t(g.ce - g.cs);
+    c.rem += uint32_t(g.ce - g.cs);
     if (g.tile < d.tiles) return true;
   }
   return false;
@@ -262,10 +283,8 @@ __device__ __forceinline__ bool cursor_next(const DecodeProblem &p, const DecSta
 // begins and does not finish.
 __device__ __forceinline__ DecodeJoin dec_join(const DecodeProblem &p, const DecStart &st, const DecCursor &at,
                                                const DecBatch &d, const DecSeg &seg, const DecRows &v, int slot) {
-  // the group that owns the unit's last chunk
-  const int64_t x = at.pos + d.chunks - 1;
-  const int last = int(((x + 1) * st.groups - 1) / st.total);
-  return {d.q.tok0, p.cu_q ? 0 : at.b, seg.hh, v.t0, v.first, v.rows, last - int(blockIdx.x) / p.group + 1, slot};
+  const int last = int(dec_owner(st, at.pos + uint32_t(d.chunks - 1)));
+  return {d.q.tok0, p.cu_q ? 0 : at.b, seg.hh, v.t0, v.first, v.rows, last - int(blockIdx.x / unsigned(p.group)) + 1, slot};
 }
 
 }  // namespace

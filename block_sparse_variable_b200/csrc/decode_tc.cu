@@ -6,12 +6,13 @@
 // One block per SM.  TMA loads of 128-token chunks of K and V through
 // three-stage rings (warps 8 and 10); S = Q K^T and O += P V issued by warps 11
 // and 9; two softmax warpgroups that take the chunks in turn, a thread a whole
-// row of 128 scores, each with a running maximum, sum and output of its own.
+// row of 64 scores at a time, each with a running maximum, sum and output of its own.
 // Nothing in the loop passes between the two groups, and while one waits for
 // its products the other has the exponentials to itself; their states are
-// joined at the end of a segment.  (Two groups on the column halves of the
+// joined at the end of a segment.  A group's 128 columns of S are two buffers of
+// 64, so that its next scores are computed while it works on these.  (Two groups on the column halves of the
 // same chunk, as in the forward pass, met once a chunk: 2640 clocks a chunk
-// against about 1050 of products and 1024 of exponentials.)  TMEM holds two
+// against about 1050 of products and 1024 of exponentials.)  TMEM holds four
 // S / P buffers and two outputs: all 512 columns at D = 128.
 //
 // The rows of a tile are gathered (any number of heads and tokens) by the
@@ -75,15 +76,15 @@ enum : int {
   kBarKEmpty = 5,      // + K stage
   kBarVFull = 8,       // + V stage
   kBarVEmpty = 11,     // + V stage
-  kBarSFull = 14,      // + group
-  kBarPFull = 16,      // + group (one arrival per thread of the group)
-  kBarPVDone = 18,     // + group: P V is in O, and the S / P buffer is free
-  kBarXchg = 20,       // + row quarter: rendezvous of the warps on the same 32 rows
-  kBarListFull = 24,   // + list buffer
-  kBarListEmpty = 26,  // + list buffer (one arrival per reading warp)
-  kBarDrain = 28,
-  kBarDrainS = 29,
-  kNumBars = 30
+  kBarSFull = 14,      // + 2 group + half
+  kBarPFull = 18,      // + 2 group + half (one arrival per thread of the group)
+  kBarPVDone = 22,     // + 2 group + half: P V is in O, and the S / P buffer is free
+  kBarXchg = 26,       // + row quarter: rendezvous of the warps on the same 32 rows
+  kBarListFull = 30,   // + list buffer
+  kBarListEmpty = 32,  // + list buffer (one arrival per reading warp)
+  kBarDrain = 34,
+  kBarDrainS = 35,
+  kNumBars = 36
 };
 
 template <int D>
@@ -96,8 +97,8 @@ struct Layout {
   static constexpr int kBars = kV + kStages * kTileBytes;
   static constexpr int kMl = kBars + kNumBars * 8;        // [2 groups][128] maximum and sum
   static constexpr int kLists = kMl + 2 * 128 * 8;        // [2] ChunkList
-  static constexpr int kBlk = kLists + 2 * int(sizeof(ChunkList));  // [32] ints of the walking warp
-  static constexpr int kTmemPtr = kBlk + 128;
+  static constexpr int kBlk = kLists + 2 * int(sizeof(ChunkList));  // [32] ids of the walking warp
+  static constexpr int kTmemPtr = kBlk + 64;
   static constexpr int kAbort = kTmemPtr + 4;
   static constexpr int kBytes = kAbort + 4;
   static_assert(kMl % 8 == 0 && sizeof(DecScratch<kThreads>) <= 2048, "the plan's scratch");
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarVFull + s), 1);
       mbar_init(bar(kBarVEmpty + s), 1);
     }
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < 4; ++g) {
       mbar_init(bar(kBarSFull + g), 1);
       mbar_init(bar(kBarPFull + g), 128);
       mbar_init(bar(kBarPVDone + g), 1);
@@ -200,10 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  // registers: the softmax threads hold a row of 128 scores (256 x 216 + 128 x
-  // 72 = the 384 x 168 of the launch)
   if (warp >= 8) {
-    regs_dec<72>();
     if (warp == kKWarp || warp == kVWarp) {
       // --------------------------------------------------- TMA producers
       const bool is_k = warp == kKWarp;
@@ -232,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         DecCursor cursor = cursor_begin(st), here;
         DecBatch d;
         DecSeg seg;
-        int *blk = reinterpret_cast<int *>(smem_raw + L::kBlk);
+        uint16_t *blk = reinterpret_cast<uint16_t *>(smem_raw + L::kBlk);
         while (ok && cursor_next(p, st, cursor, d, seg, here)) {
           const DecRows v = dec_rows(p, d, seg.tile);
           const bool whole = seg.cs == 0 && seg.ce == d.chunks;
@@ -240,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0 && seg.cs == 0 && !whole) p.join[blockIdx.x] = dec_join(p, st, here, d, seg, v, slot);
           // the tile's query rows into L2, ahead of their gathering
           for (int r = lane; r < v.rows; r += 32) {
-            const int y = v.first + r;
+            const int y = v.first + r, z = div_gg(p, y);
             const T *q = static_cast<const T *>(p.q) + (p.cu_q ? 0 : here.b) * p.q_sb +
-                         (d.q.tok0 + v.t0 + y / p.gg) * p.q_st + int64_t(seg.hh * p.gg + y % p.gg) * p.q_sh;
+                         (d.q.tok0 + v.t0 + z) * p.q_st + int64_t(seg.hh * p.gg + y - z * p.gg) * p.q_sh;
             asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q));
             asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q + D - 8));
           }
@@ -297,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ------------------------------------------------------ MMA issuers
-      constexpr uint32_t idS = idesc_f16(BF16, 128, 128, false, false);
+      constexpr uint32_t idS = idesc_f16(BF16, 128, 64, false, false);
       constexpr uint32_t idPV = idesc_f16(BF16, 128, D, false, true);
       const uint64_t dQ = sw128_desc(sQ, 16, 1024);
       const uint64_t dK = sw128_desc(sK, 16, 1024);
@@ -309,14 +307,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           each_chunk([&](int, int) {
             const uint32_t t = kv_it, g = t & 1u;
             const int sg = int(t % kStages);
-            if (t >= 2 && !(ok = wait_warp(bar(kBarPVDone + g), (t / 2 - 1) & 1u, abort, status))) return;
             if (!(ok = wait_warp(bar(kBarKFull + sg), (t / kStages) & 1u, abort, status))) return;
-            tc_fence_after();
-            const uint32_t da = tS0 + g * 128u;
-            const uint64_t ka = dK + uint64_t(sg * (L::kTileBytes >> 4));
+#pragma unroll 1
+            for (uint32_t h = 0; h < 2; ++h) {
+              if (t >= 2 && !(ok = wait_warp(bar(kBarPVDone + 2 * g + h), (t / 2 - 1) & 1u, abort, status))) return;
+              tc_fence_after();
+              const uint32_t da = tS0 + g * 128u + h * 64u;
+              const uint64_t ka = dK + uint64_t(sg * (L::kTileBytes >> 4)) + uint64_t(h * 512u);  // 64 rows of 128 B
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) mma_ss_e(da, dQ + kstep(kk), ka + kstep(kk), idS, kk > 0 ? 1u : 0u);
-            mma_commit_e(bar(kBarSFull + g));
+              for (int kk = 0; kk < D / 16; ++kk) mma_ss_e(da, dQ + kstep(kk), ka + kstep(kk), idS, kk > 0 ? 1u : 0u);
+              mma_commit_e(bar(kBarSFull + 2 * g + h));
+            }
             mma_commit_e(bar(kBarKEmpty + sg));
             ++kv_it;
           });
@@ -330,19 +331,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t t = kv_it, g = t & 1u;
             const int sg = int(t % kStages);
             if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
-            if (!(ok = wait_warp(bar(kBarPFull + g), (t / 2) & 1u, abort, status))) return;
-            tc_fence_after();
-            const uint32_t pa = tS0 + g * 128u, da = tO0 + g * uint32_t(D);  // 16 kv rows of P are 8 columns
-            const uint64_t vd = dV + uint64_t(sg * (L::kTileBytes >> 4));
-            uint32_t on = g ? acc[1] : acc[0];
+#pragma unroll 1
+            for (uint32_t h = 0; h < 2; ++h) {
+              if (!(ok = wait_warp(bar(kBarPFull + 2 * g + h), (t / 2) & 1u, abort, status))) return;
+              tc_fence_after();
+              // 16 kv rows of P are 8 columns, of V 2 KB
+              const uint32_t pa = tS0 + g * 128u + h * 64u, da = tO0 + g * uint32_t(D);
+              const uint64_t vd = dV + uint64_t(sg * (L::kTileBytes >> 4)) + uint64_t(h * 512u);
+              uint32_t on = g ? acc[1] : acc[0];
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              mma_ts_e(da, pa + uint32_t(8 * kk), vd + uint64_t(kk * 128), idPV, on);
-              on = 1;
+              for (int kk = 0; kk < 4; ++kk) {
+                mma_ts_e(da, pa + uint32_t(8 * kk), vd + uint64_t(kk * 128), idPV, on);
+                on = 1;
+              }
+              if (g) acc[1] = 1;
+              else acc[0] = 1;
+              mma_commit_e(bar(kBarPVDone + 2 * g + h));
             }
-            if (g) acc[1] = 1;
-            else acc[0] = 1;
-            mma_commit_e(bar(kBarPVDone + g));
             mma_commit_e(bar(kBarVEmpty + sg));
             ++kv_it;
           });
@@ -357,7 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // --------------------------------------------- softmax warpgroups
-    regs_inc<216>();
     const int wg = warp >> 2;
     const int r = tid & 127;  // tile row = TMEM lane
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
@@ -381,10 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4 x[kRounds];
 #pragma unroll
       for (int i = 0; i < kRounds; ++i) {
-        const int rr = tid / kPieces + i * (kSoftmaxThreads / kPieces), y = first + rr;
+        const int rr = tid / kPieces + i * (kSoftmaxThreads / kPieces), y = first + rr, z = div_gg(p, y);
         x[i] = make_uint4(0, 0, 0, 0);
         if (rr < rows)
-          x[i] = __ldg(reinterpret_cast<const uint4 *>(q + int64_t(y / p.gg) * p.q_st + int64_t(h0 + y % p.gg) * p.q_sh) + c);
+          x[i] = __ldg(reinterpret_cast<const uint4 *>(q + int64_t(z) * p.q_st + int64_t(h0 + y - z * p.gg) * p.q_sh) + c);
       }
       if (!(ok = wait_warp(bar(kBarQEmpty), (seg_n & 1u) ^ 1u, abort, status))) return;
       ++seg_n;
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kvlen = g.kvlen, qbase = kvlen - g.qlen, qb = g.b, slot = g.slot;
       const bool live = r < g.rows;
       const int xr = g.first + min(r, g.rows - 1);
-      const int tq = g.t0 + xr / p.gg, row = g.tok0 + tq, head = g.hh * p.gg + xr % p.gg;
+      const int z = div_gg(p, xr), tq = g.t0 + z, row = g.tok0 + tq, head = g.hh * p.gg + xr - z * p.gg;
       const int64_t *bits = p.tree ? p.tree + qb * p.t_sb + int64_t(row) * p.t_st : nullptr;
       // the columns [u, u + 64) that the row sees
       auto visible = [&](int u) {
@@ -419,8 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       each_chunk([&](const int u0c, int) {
         const uint32_t t = kv_it++;
         if (int(t & 1u) != wg) return;
-        if (!(ok = wait_warp(bar(kBarSFull + wg), (t / 2) & 1u, abort, status))) return;
-        tc_fence_after();
         const int valid_all = kvlen - u0c;
         if (valid_all < 128) {
           // rows past the used length may hold anything: their weights are 0,
@@ -435,60 +437,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        uint32_t x[128];
-        tmem_ld_cols<128>(tS, x);
-        tmem_wait_ld();
-        if (u0c + kChunk > edge_from) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int buf = 2 * wg + h;
+          if (!(ok = wait_warp(bar(kBarSFull + buf), (t / 2) & 1u, abort, status))) return;
+          tc_fence_after();
+          uint32_t x[64];
+          tmem_ld_cols<64>(tS + uint32_t(64 * h), x);
+          tmem_wait_ld();
+          if (u0c + 64 * h + 64 > edge_from) {
             const uint64_t vis = visible(u0c + 64 * h);
             const uint32_t lo = uint32_t(vis), hi = uint32_t(vis >> 32);
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (!((c < 32 ? lo : hi) & (1u << (c & 31)))) x[64 * h + c] = __float_as_uint(-INFINITY);
+              if (!((c < 32 ? lo : hi) & (1u << (c & 31)))) x[c] = __float_as_uint(-INFINITY);
           }
-        }
-        float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; ++c) pm[c & 3] = fmaxf(pm[c & 3], __uint_as_float(x[c]));
-        const float cm = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * p.scale_log2;
-        const bool move = cm > m + kSlack;  // (true for a first finite maximum)
-        if (__any_sync(0xffffffffu, move)) {
-          const float m_new = move ? cm : m;
-          const float alpha = move ? ex2(m - m_new) : 1.f;
-          m = m_new;
-          l *= alpha;
-          if (n > 0) {  // the product before is in O: this S waited for it
+          for (int c = 0; c < 64; ++c) pm[c & 3] = fmaxf(pm[c & 3], __uint_as_float(x[c]));
+          const float cm = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * p.scale_log2;
+          const bool move = cm > m + kSlack;  // (true for a first finite maximum)
+          if (__any_sync(0xffffffffu, move)) {
+            const float m_new = move ? cm : m;
+            const float alpha = move ? ex2(m - m_new) : 1.f;
+            m = m_new;
+            l *= alpha;
+            if (n + h > 0) {  // the products so far must be in O
+              const uint32_t k = t / 2 - (h ? 0u : 1u);  // the group's chunk of the half before this one
+              if (!(ok = wait_warp(bar(kBarPVDone + 2 * wg + (h ^ 1)), k & 1u, abort, status))) return;
+              tc_fence_after();
+#pragma unroll 1
+              for (int j = 0; j < D / 32; ++j) {
+                uint32_t o[32];
+                tmem_ld32(tO + uint32_t(32 * j), o);
+                tmem_wait_ld();
 #pragma unroll
-            for (int h = 0; h < D / 32; ++h) {
-              uint32_t o[32];
-              tmem_ld32(tO + uint32_t(32 * h), o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-              tmem_st32(tO + uint32_t(32 * h), o);
+                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                tmem_st32(tO + uint32_t(32 * j), o);
+              }
             }
           }
-        }
-        const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: every weight is 0
-        float2 ps[2] = {{0.f, 0.f}, {0.f, 0.f}};
-        const float2 sc = {p.scale_log2, p.scale_log2}, mm = {-ref, -ref};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: every weight is 0
+          float2 ps[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          const float2 sc = {p.scale_log2, p.scale_log2}, mm = {-ref, -ref};
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float2 a = fma2(make_float2(__uint_as_float(x[64 * h + c]), __uint_as_float(x[64 * h + c + 1])), sc, mm);
+            const float2 a = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc, mm);
             const float2 e = {ex2(a.x), ex2(a.y)};
             ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], e);
             pk[c >> 1] = Pack2<T>::pack(e.x, e.y);
           }
-          tmem_st32(tS + uint32_t(32 * h), pk);  // the whole row of S is in registers
+          tmem_st32(tS + uint32_t(64 * h), pk);  // over its own S, which is in registers
+          l += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kBarPFull + buf));
         }
-        l += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(kBarPFull + wg));
         ++n;
       });
       if (!ok) break;
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // w writes half of the columns from both groups' outputs
       if (n > 0) {
         const uint32_t t = kv_it - 1 - uint32_t(int((kv_it - 1) & 1u) != wg);  // this group's last chunk
-        if (!(ok = wait_warp(bar(kBarPVDone + wg), (t / 2) & 1u, abort, status))) break;
+        if (!(ok = wait_warp(bar(kBarPVDone + 2 * wg + 1), (t / 2) & 1u, abort, status))) break;
       }
       s_ml[wg * 128 + r] = make_float2(m, l);
       if (!rendezvous()) break;
