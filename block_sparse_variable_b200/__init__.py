@@ -1,7 +1,8 @@
 """Block-sparse variable-length FlashAttention for B200 (sm_100a).
 
 Thin ctypes binding over the C ABI in ``include/bsa.h`` (``libbsa.so``,
-built in-tree by ``block_sparse_variable_b200/build.py``).  The functions keep
+built in-tree by ``block_sparse_variable_b200/build.py``, with ``_binding.so``
+for the calls of the cache operators).  The functions keep
 the C names; they only marshal torch tensors into ``bsa_tensor``
 descriptors, allocate outputs / workspace with torch when the caller does
 not pass them, and raise ``BsaError`` on a non-OK status.  Every step of
@@ -67,6 +68,9 @@ def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           f"`python block_sparse_variable_b200/build.py` (nvcc, sm_100a)")
+    if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+        raise ImportError(f"{_HERE}/_binding.so is missing: build it with "
+                          f"`python block_sparse_variable_b200/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     T = ctypes.POINTER(bsa_tensor)
     Pp = ctypes.POINTER(bsa_params)
@@ -420,73 +424,49 @@ def bsa_fwd_static_workspace(q, k, v, index, params: Params, *, cu_seqlens_q=Non
 
 
 # ---------------------------------------------------------- cache operators
-# A decoding step makes one call for a few microseconds of GPU work, so these
-# marshal all descriptors of a call into one buffer.
-_TENSOR = struct.Struct("Qii4q4q")  # bsa_tensor
+# A decoding step makes these calls for a few microseconds of GPU work each, so
+# the native module _binding describes their tensors and makes the call.
+from . import _binding  # noqa: E402  (needs torch loaded)
+
 _PARAMS = struct.Struct("iiqqqqdiiii")  # bsa_params, padded to its alignment
-assert _TENSOR.size == ctypes.sizeof(bsa_tensor) and _PARAMS.size == ctypes.sizeof(bsa_params)
-_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+assert _PARAMS.size == ctypes.sizeof(bsa_params)
 
 
-def _marshal(params: Params, tensors):
-    """(buffer, address of the bsa_params, addresses of the tensors, None for
-    the absent); the addresses hold while the buffer does."""
-    buf = ctypes.create_string_buffer(_PARAMS.size + _TENSOR.size * len(tensors))
-    base = ctypes.addressof(buf)
+def _entry(name: str):
+    return (ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value,
+            ctypes.cast(getattr(_lib, name + "_get_workspace"), ctypes.c_void_p).value)
+
+
+_OPS = {name: (op, *_entry(name), name) for op, name in
+        enumerate(("bsa_block_means", "bsa_select_blocks", "bsa_decode"))}
+
+
+def _call(name: str, params: Params, tensors, extra, workspace, stream):
+    """One call on the tensors' device; returns the workspace."""
+    op, fn, fn_ws, _ = _OPS[name]
     p = params
-    _PARAMS.pack_into(buf, 0, LAYOUTS[p.q_layout], LAYOUTS[p.kv_layout], p.num_heads, p.num_kv_heads,
-                      p.block_shape[0], p.block_shape[1], p.scale, 1 if p.return_lse else 0,
-                      1 if p.causal else 0, 1 if p.deterministic else 0, 0)
-    at, refs = _PARAMS.size, []
-    for t in tensors:
-        if t is None:
-            refs.append(None)
-            continue
-        n = t.dim()
-        if n > 4:
-            raise ValueError("at most 4 dimensions")
-        pad = _PAD[n]
-        _TENSOR.pack_into(buf, at, t.data_ptr() or (_EMPTY_PTR if t.numel() == 0 else 0),
-                          _DTYPES.get(t.dtype, 0), n, *t.shape, *pad, *t.stride(), *pad)
-        refs.append(base + at)
-        at += _TENSOR.size
-    return buf, base, refs
+    prm = _PARAMS.pack(LAYOUTS[p.q_layout], LAYOUTS[p.kv_layout], p.num_heads, p.num_kv_heads, p.block_shape[0],
+                       p.block_shape[1], p.scale, 1 if p.return_lse else 0, 1 if p.causal else 0,
+                       1 if p.deterministic else 0, 0)
+    st, sizing, ws = _binding.call(op, fn, fn_ws, prm, tensors, extra, workspace,
+                                   None if stream is None else _stream(stream))
+    if st:
+        raise BsaError(st, name + "_get_workspace" if sizing else name)
+    return ws
 
 
-def _run_on(dev: int, workspace, size, call, stream, where, tensors):
-    """Checks devices, finds the workspace (`size()` bytes when the caller has
-    none) and makes `call(workspace, bytes, stream)` on the tensors' device."""
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{where}: all tensors must be on one CUDA device")
-    if dev < 0:
-        raise ValueError(f"{where}: the tensors must be on a CUDA device")
-    if workspace is None:
-        workspace = torch.empty(max(size(), 256), dtype=torch.uint8, device=tensors[0].device)
-    elif workspace.get_device() != dev:
-        raise ValueError(f"{where}: the workspace must be on the tensors' device")
-    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-    n = workspace.numel() * workspace.element_size()
-    if torch.cuda.current_device() == dev:
-        st = call(workspace.data_ptr(), n, s)
-    else:
-        with torch.cuda.device(dev):
-            st = call(workspace.data_ptr(), n, s)
-    _check(st, where)
-    return workspace
-
-
-def _means_size(refs, prm) -> int:
-    n = ctypes.c_size_t(0)
-    _check(_lib.bsa_block_means_get_workspace(*refs[:5], prm, refs[5], ctypes.byref(n)),
-           "bsa_block_means_get_workspace")
+def _size(name: str, params: Params, tensors, at: int, *extra) -> int:
+    """Workspace bytes; the params stand before tensor `at` of the C call."""
+    refs = [_ref(describe(t)) for t in tensors]
+    n, cp = ctypes.c_size_t(0), params.c()
+    _check(getattr(_lib, name)(*refs[:at], ctypes.byref(cp), *extra, *refs[at:], ctypes.byref(n)), name)
     return n.value
 
 
 def bsa_block_means_get_workspace(k, means, params: Params, *, cu_seqlens_kv=None, seqused_kv=None,
                                   block_table=None, first_kv=None) -> int:
-    buf, prm, refs = _marshal(params, (k, cu_seqlens_kv, seqused_kv, block_table, first_kv, means))
-    return _means_size(refs, prm)
+    return _size("bsa_block_means_get_workspace", params,
+                 (k, cu_seqlens_kv, seqused_kv, block_table, first_kv, means), 5)
 
 
 def bsa_block_means(k, params: Params, *, cu_seqlens_kv=None, seqused_kv=None, block_table=None,
@@ -503,25 +483,16 @@ def bsa_block_means(k, params: Params, *, cu_seqlens_kv=None, seqused_kv=None, b
         else:
             B, most = k.shape[0], k.shape[2]
         means = torch.zeros(B, N2, -(-most // bkv), k.shape[-1], dtype=k.dtype, device=k.device)
-    tensors = (k, cu_seqlens_kv, seqused_kv, block_table, first_kv, means)
-    buf, prm, refs = _marshal(params, tensors)
-    workspace = _run_on(k.get_device(), workspace, lambda: _means_size(refs, prm),
-                        lambda w, n, s: _lib.bsa_block_means(*refs[:5], prm, refs[5], w, n, s),
-                        stream, "bsa_block_means", tensors)
+    workspace = _call("bsa_block_means", params, (k, cu_seqlens_kv, seqused_kv, block_table, first_kv, means),
+                      (0, 0), workspace, stream)
     return means, workspace
-
-
-def _select_size(refs, prm, sink, local) -> int:
-    n = ctypes.c_size_t(0)
-    _check(_lib.bsa_select_blocks_get_workspace(*refs[:5], prm, sink, local, refs[5], ctypes.byref(n)),
-           "bsa_select_blocks_get_workspace")
-    return n.value
 
 
 def bsa_select_blocks_get_workspace(q, means, index, params: Params, *, sink_blocks=0, local_blocks=0,
                                     cu_seqlens_q=None, cu_seqlens_kv=None, seqused_kv=None) -> int:
-    buf, prm, refs = _marshal(params, (q, means, cu_seqlens_q, cu_seqlens_kv, seqused_kv, index))
-    return _select_size(refs, prm, int(sink_blocks), int(local_blocks))
+    return _size("bsa_select_blocks_get_workspace", params,
+                 (q, means, cu_seqlens_q, cu_seqlens_kv, seqused_kv, index), 5, int(sink_blocks),
+                 int(local_blocks))
 
 
 def bsa_select_blocks(q, means, params: Params, *, width=None, index_heads=None, rows=None,
@@ -546,20 +517,9 @@ def bsa_select_blocks(q, means, params: Params, *, width=None, index_heads=None,
             B = cu_seqlens_q.shape[0] - 1
             most = min(q.shape[0], q.shape[0] // bq + B)
             index = torch.full((H, most, width), -1, dtype=torch.int16, device=q.device).view(torch.uint16)
-    sink, local = int(sink_blocks), int(local_blocks)
-    tensors = (q, means, cu_seqlens_q, cu_seqlens_kv, seqused_kv, index)
-    buf, prm, refs = _marshal(params, tensors)
-    workspace = _run_on(q.get_device(), workspace, lambda: _select_size(refs, prm, sink, local),
-                        lambda w, n, s: _lib.bsa_select_blocks(*refs[:5], prm, sink, local, refs[5], w, n, s),
-                        stream, "bsa_select_blocks", tensors)
+    workspace = _call("bsa_select_blocks", params, (q, means, cu_seqlens_q, cu_seqlens_kv, seqused_kv, index),
+                      (int(sink_blocks), int(local_blocks)), workspace, stream)
     return index, workspace
-
-
-def _decode_size(refs, prm) -> int:
-    n = ctypes.c_size_t(0)
-    _check(_lib.bsa_decode_get_workspace(*refs[:9], prm, refs[9], refs[10], ctypes.byref(n)),
-           "bsa_decode_get_workspace")
-    return n.value
 
 
 def bsa_decode_get_workspace(q, k, v, params: Params, *, index=None, tree_mask=None, cu_seqlens_q=None,
@@ -568,9 +528,8 @@ def bsa_decode_get_workspace(q, k, v, params: Params, *, index=None, tree_mask=N
     out = q if out is None else out
     if lse is None and params.return_lse:
         lse = torch.empty(_lse_shape(q, params), dtype=torch.float32)
-    buf, prm, refs = _marshal(params, (q, k, v, index, tree_mask, cu_seqlens_q, cu_seqlens_kv,
-                                       seqused_kv, block_table, out, lse))
-    return _decode_size(refs, prm)
+    return _size("bsa_decode_get_workspace", params,
+                 (q, k, v, index, tree_mask, cu_seqlens_q, cu_seqlens_kv, seqused_kv, block_table, out, lse), 9)
 
 
 def bsa_decode(q, k, v, params: Params, *, index=None, tree_mask=None, cu_seqlens_q=None,
@@ -582,10 +541,7 @@ def bsa_decode(q, k, v, params: Params, *, index=None, tree_mask=None, cu_seqlen
     if out is None:
         out = torch.empty_like(q)
     if lse is None and params.return_lse:
-        lse = torch.empty(_lse_shape(q, params), dtype=torch.float32, device=q.device)
-    tensors = (q, k, v, index, tree_mask, cu_seqlens_q, cu_seqlens_kv, seqused_kv, block_table, out, lse)
-    buf, prm, refs = _marshal(params, tensors)
-    workspace = _run_on(q.get_device(), workspace, lambda: _decode_size(refs, prm),
-                        lambda w, n, s: _lib.bsa_decode(*refs[:9], prm, refs[9], refs[10], w, n, s),
-                        stream, "bsa_decode", tensors)
+        lse = q.new_empty(_lse_shape(q, params), dtype=torch.float32)
+    workspace = _call("bsa_decode", params, (q, k, v, index, tree_mask, cu_seqlens_q, cu_seqlens_kv, seqused_kv,
+                                             block_table, out, lse), (0, 0), workspace, stream)
     return out, lse, workspace

@@ -1,4 +1,5 @@
-"""Builds libbsa.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Builds libbsa.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_binding.so (the native part of the Python binding) with the host compiler."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -6,12 +7,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbsa.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -35,11 +38,15 @@ def _headers():
     return hs
 
 
-def _stale(obj, src):
-    if not os.path.exists(obj):
+def _stale_file(out, inputs):
+    if not os.path.exists(out):
         return True
-    t = os.path.getmtime(obj)
-    return any(os.path.getmtime(x) > t for x in [src] + _headers())
+    t = os.path.getmtime(out)
+    return any(os.path.getmtime(x) > t for x in inputs)
+
+
+def _stale(obj, src):
+    return _stale_file(obj, [src] + _headers())
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -73,7 +80,31 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([cc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and not _stale_file(BINDING, [src, os.path.join(INCLUDE, "bsa.h")]):
+        return BINDING
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o", tmp,
+           # torch's own libraries: found by name, torch being loaded first
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("the host compiler failed for binding.cpp")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
