@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "cache.h"
+#include "cp_async.cuh"
 #include "decode_plan.cuh"
 #include "launch.cuh"
 #include "pack16.cuh"
@@ -41,15 +42,6 @@ struct Smem {
   static_assert(kWarps * kTile * D * 4 <= kWarps * kRing, "the states are joined in the ring's memory");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
-  const int n = in ? 16 : 0;  // 0: the 16 bytes are zeros and nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
