@@ -32,6 +32,12 @@ struct MeansProblem {
   uint32_t *status;
 };
 
+// an index row whose scores are too close for 32 bits
+struct SelectAgain {
+  int32_t r, hi;
+  uint32_t lo, up;  // keys between which blocks are scored again
+};
+
 struct SelectProblem {
   KvWhere kv;  // lengths only: no table, no cache
   int32_t q_layout, B, N1, N2, D, g, Hidx, BQ, BKV, NB, W, R, Rg, dtype, causal;
@@ -45,9 +51,12 @@ struct SelectProblem {
   int64_t ix_s0, ix_s1, ix_s2;
   uint32_t *status;
   int32_t *row_nk;     // [Rg] blocks that the index row may choose from, -1: no such row
-  int32_t *row_batch;  // [Rg]
-  double *qsum;        // [Hidx][Rg][D] sums of the query rows of a row's block
-  uint64_t *keys;      // [Hidx][Rg][NB] order-preserving bits of the scores
+  int32_t *row_batch, *row_block;  // [Rg] its sequence, and its query block there
+  float *qsum;         // [Hidx][Rg][D] sums of the query rows of a row's block
+  float *bound;        // [Hidx][Rg] what bounds their errors (select.cu)
+  uint64_t *keys;      // [Hidx][Rg][NB] scores
+  uint32_t *again_count;
+  SelectAgain *again;  // [Hidx * Rg]
 };
 
 // a unit that a decode block begins and others finish: what the join kernel reads

@@ -197,7 +197,7 @@ bsa_status prepare_means(const bsa_tensor *k, const bsa_tensor *cu_kv, const bsa
 
 // ---------------------------------------------------------- block selection
 struct SelectRegions {
-  bsa_ws_region status, row_nk, row_batch, qsum, keys;
+  bsa_ws_region status, row_nk, row_batch, row_block, qsum, bound, keys, again_count, again;
 };
 
 bsa_status prepare_select(const bsa_tensor *q, const bsa_tensor *means, const bsa_tensor *cu_q,
@@ -247,8 +247,12 @@ bsa_status prepare_select(const bsa_tensor *q, const bsa_tensor *means, const bs
   place(cur, kStWords * 4, L.status);
   place(cur, uint64_t(Rg) * 4, L.row_nk);
   place(cur, uint64_t(Rg) * 4, L.row_batch);
-  place(cur, uint64_t(H) * Rg * D * 8, L.qsum);
+  place(cur, uint64_t(Rg) * 4, L.row_block);
+  place(cur, uint64_t(H) * Rg * D * 4, L.qsum);
+  place(cur, uint64_t(H) * Rg * 4, L.bound);
   place(cur, uint64_t(H) * Rg * NB * 8, L.keys);
+  place(cur, 4, L.again_count);
+  place(cur, uint64_t(H) * Rg * sizeof(SelectAgain), L.again);
   bytes = round256(cur);
   return BSA_OK;
 }
@@ -399,8 +403,12 @@ bsa_status bsa_select_blocks(const bsa_tensor *q, const bsa_tensor *means, const
   p.status = at<uint32_t>(workspace, L.status);
   p.row_nk = at<int32_t>(workspace, L.row_nk);
   p.row_batch = at<int32_t>(workspace, L.row_batch);
-  p.qsum = at<double>(workspace, L.qsum);
+  p.row_block = at<int32_t>(workspace, L.row_block);
+  p.qsum = at<float>(workspace, L.qsum);
+  p.bound = at<float>(workspace, L.bound);
   p.keys = at<uint64_t>(workspace, L.keys);
+  p.again_count = at<uint32_t>(workspace, L.again_count);
+  p.again = at<SelectAgain>(workspace, L.again);
   return launch_select_blocks(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

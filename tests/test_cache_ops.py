@@ -245,16 +245,30 @@ def test_select_ties_infinities_and_nan(W, kvlen):
 
 
 @gpu
-def test_select_close_scores_are_ordered():
+@pytest.mark.parametrize("T", [1, 200])
+def test_select_close_scores_are_ordered(T):
     """Two blocks whose scores differ by 1 part in 10^9."""
-    s = C.make(qlens=(1,), kvlens=(512,), N1=1, N2=1, D=64, dtype=FP, poison=False)
+    s = C.make(qlens=(T,), kvlens=(512,), N1=1, N2=1, D=64, dtype=FP, poison=False, tail_rows=0)
     s.q[:] = 1.0
-    s.q[0, 0, 1] = 2.0 ** -10
+    s.q[:, 0, 1] = 2.0 ** -10
     m = torch.zeros(1, 1, 4, 64, dtype=FP, device="cuda")
     m[0, 0, :, 0] = 1024.0
     m[0, 0, 2, 1] = 2.0 ** -12
     index, _ = _select(s, m, dict(W=1))
-    assert index.to(torch.int32).item() == 2
+    assert (index.to(torch.int32) == 2).all()
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 150])
+@pytest.mark.parametrize("dtype, scale", [(BF, 1e37), (BF, 1e-37), (FP, 6e4), (FP, 1e-7)])
+def test_select_at_the_ends_of_the_range(T, dtype, scale):
+    """Products that pass 32-bit floats, and values below the normal ones."""
+    s = C.make(qlens=(T, T), kvlens=(5000, 2600), N1=4, N2=2, D=64, dtype=dtype, seed=13, poison=False, tail_rows=0)
+    s.qd = [(x.double() * scale).clamp(-torch.finfo(dtype).max, torch.finfo(dtype).max).to(dtype) for x in s.qd]
+    s.q = torch.cat(s.qd).cuda()
+    means = (torch.randn(s.B, s.N2, s.NB, s.D, generator=s.g).double() * scale / 8).to(dtype).cuda()
+    index, _ = _select(s, means, dict(W=7))
+    assert torch.equal(_as_rows(s, index), C.ref_select(s, means, 7, "group").int())
 
 
 @gpu
