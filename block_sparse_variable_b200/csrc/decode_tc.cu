@@ -43,10 +43,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = 128, kChunk = 128;
+constexpr int kRows = 128, kChunk = 128;  // rows of a softmax group, tokens of a chunk
 constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kStages = 3;
 constexpr int kKWarp = 8, kPvWarp = 9, kVWarp = 10, kSWarp = 11;
 // a row's reference maximum moves once a score passes it by 2^8: weights stay
 // below 2^8, and the output is rarely rescaled
@@ -87,14 +86,19 @@ enum : int {
   kNumBars = 36
 };
 
-template <int D>
+// Pair: a tile of 256 rows, a group of 128 each, both of which take every chunk;
+// else a tile of 128 rows, whose chunks the groups take in turn.
+template <int D, bool kPair>
 struct Layout {
+  static constexpr int kTile = kPair ? 2 * kRows : kRows;
+  // at D = 128 seven 32 KB tiles of Q, K and V fill the shared memory
+  static constexpr int kKStages = 3, kVStages = kPair ? 2 : 3;
   static constexpr int kBox = 128 * 128;  // 128 rows of 64 columns
   static constexpr int kTileBytes = D / 64 * kBox;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + kTileBytes;
-  static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kBars = kV + kStages * kTileBytes;
+  static constexpr int kK = kQ + (kPair ? 2 : 1) * kTileBytes;
+  static constexpr int kV = kK + kKStages * kTileBytes;
+  static constexpr int kBars = kV + kVStages * kTileBytes;
   static constexpr int kMl = kBars + kNumBars * 8;        // [2 groups][128] maximum and sum
   static constexpr int kLists = kMl + 2 * 128 * 8;        // [2] ChunkList
   static constexpr int kBlk = kLists + 2 * int(sizeof(ChunkList));  // [32] ids of the walking warp
@@ -116,40 +120,30 @@ __device__ __forceinline__ uint64_t tree_bits(const DecodeProblem &p, const int6
 }
 __device__ __forceinline__ uint64_t low_bits(int64_t n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull; }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     k_decode_tc(const DecodeProblem p, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
-  using L = Layout<D>;
+  using L = Layout<D, kPair>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   extern __shared__ unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  griddep_wait();
-  griddep_launch_next();
   uint32_t *status = p.flags + blockIdx.x;  // this block's flags
   const uint32_t base = smem_u32(smem_raw);
-  uint32_t len_flags = 0;
-  // (the states' memory serves as scratch here; nothing is in static shared
-  // memory, so that the tiles start at the 1024-byte aligned window)
-  const DecStart st = dec_start<kThreads>(p, *reinterpret_cast<DecScratch<kThreads> *>(smem_raw + L::kMl), len_flags);
-  if (tid == 0) {
-    *status = base & 1023u ? BSA_FLAG_INTERNAL : 0u;  // swizzled tiles need a 1024-byte aligned base
-    p.join[blockIdx.x] = DecodeJoin{};
-    __threadfence();
-  }
-  __syncthreads();
-  if (len_flags) atomicOr(status, len_flags);
-  if ((base & 1023u) || st.lo >= st.hi) return;  // the whole block
+  const bool aligned = (base & 1023u) == 0;  // swizzled tiles need a 1024-byte aligned base
   const uint32_t sQ = base + L::kQ, sK = base + L::kK, sV = base + L::kV;
   auto bar = [&](int i) { return base + L::kBars + 8u * uint32_t(i); };
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem_raw + L::kTmemPtr);
   volatile int *abort = reinterpret_cast<volatile int *>(smem_raw + L::kAbort);
   volatile ChunkList *lists = reinterpret_cast<volatile ChunkList *>(smem_raw + L::kLists);
 
+  // what needs no data comes before the wait for the kernel before this one
   if (tid == 0) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
     mbar_init(bar(kBarQFull), kSoftmaxThreads);
     mbar_init(bar(kBarQEmpty), 1);
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < 3; ++s) {
       mbar_init(bar(kBarKFull + s), 1);
       mbar_init(bar(kBarKEmpty + s), 1);
       mbar_init(bar(kBarVFull + s), 1);
@@ -157,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 4; ++g) {
       mbar_init(bar(kBarSFull + g), 1);
-      mbar_init(bar(kBarPFull + g), 128);
+      mbar_init(bar(kBarPFull + g), kRows);
       mbar_init(bar(kBarPVDone + g), 1);
     }
     for (int q = 0; q < 4; ++q) mbar_init(bar(kBarXchg + q), kSoftmaxThreads / 4);
@@ -170,13 +164,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     fence_barrier_init();
   }
-  if (warp == kPvWarp) {
+  if (warp == kPvWarp && aligned) {
     tmem_alloc(base + L::kTmemPtr, 512);
     tmem_relinquish();
+  }
+  griddep_wait();
+  griddep_launch_next();
+  uint32_t len_flags = 0;
+  // (the states' memory serves as scratch here; nothing is in static shared
+  // memory, so that the tiles start at the aligned window)
+  const DecStart st = dec_start<kThreads>(p, *reinterpret_cast<DecScratch<kThreads> *>(smem_raw + L::kMl), len_flags);
+  if (tid == 0) {
+    *status = aligned ? 0u : BSA_FLAG_INTERNAL;
+    p.join[blockIdx.x] = DecodeJoin{};
+    __threadfence();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (len_flags) atomicOr(status, len_flags);
+  if (!aligned) return;  // the whole block
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS0 = tmem, tO0 = tmem + 256u;
 
@@ -206,13 +213,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // --------------------------------------------------- TMA producers
       const bool is_k = warp == kKWarp;
       const CUtensorMap *map = is_k ? &map_k : &map_v;
-      if (lane == 0) tma_prefetch_desc(map);
       const uint32_t ring = is_k ? sK : sV;
       const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
-      int armed[kStages] = {-1, -1, -1};
+      const int stages = is_k ? L::kKStages : L::kVStages;
+      int armed[3] = {-1, -1, -1}, s = 0;
+      uint32_t ph = 0;
       auto load = [&](int u, int pg, const volatile SegInfo &g) {
-        const int s = int(kv_it % kStages);
-        const uint32_t ph = (kv_it / kStages) & 1u;
         if (!(ok = wait_warp(bar(empty0 + s), ph ^ 1u, abort, status))) return;
         if (lane == 0) {
           int row, last;  // tile coordinates: (0, row, 0, h2, last)
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_5d(ring + s * L::kTileBytes, map, bar(full0 + s), 0, row, 0, g.h2, last);
         }
         armed[s] = int(ph);
-        ++kv_it;
+        if (++s == stages) s = 0, ph ^= 1u;
       };
       if (is_k) {
         uint32_t flags = 0;
@@ -289,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (*abort && lane == 0) {  // let every copy already issued land before the block exits
-        for (int s = 0; s < kStages; ++s)
-          if (armed[s] >= 0) drain_wait(bar(full0 + s), uint32_t(armed[s]));
+        for (int i = 0; i < 3; ++i)
+          if (armed[i] >= 0) drain_wait(bar(full0 + i), uint32_t(armed[i]));
       }
       __syncwarp();
     } else {
@@ -301,39 +307,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dK = sw128_desc(sK, 16, 1024);
       const uint64_t dV = sw128_desc(sV, L::kBox, 1024);
       auto kstep = [](int kk) { return uint64_t((kk >> 2) * (L::kBox >> 4) + (kk & 3) * 2); };
+      // the groups that take the chunk, as bits, and chunks that each has taken
+      uint32_t done[2] = {0, 0};
+      auto groups = [&](const volatile SegInfo &g) { return kPair ? (g.rows > kRows ? 3u : 1u) : 1u << (kv_it & 1u); };
       if (warp == kSWarp) {
-        for (uint32_t q_it = 0; next_segment(); ++q_it) {
+        uint32_t q_it = 0;
+        for (const volatile ChunkList *list; (list = next_segment()) != nullptr; ++q_it) {
+          const uint32_t both = groups(list->seg);
           if (!(ok = wait_warp(bar(kBarQFull), q_it & 1u, abort, status))) break;
           each_chunk([&](int, int) {
-            const uint32_t t = kv_it, g = t & 1u;
-            const int sg = int(t % kStages);
-            if (!(ok = wait_warp(bar(kBarKFull + sg), (t / kStages) & 1u, abort, status))) return;
+            const uint32_t t = kv_it, act = kPair ? both : 1u << (t & 1u);
+            const int sg = int(t % L::kKStages);
+            if (!(ok = wait_warp(bar(kBarKFull + sg), (t / L::kKStages) & 1u, abort, status))) return;
 #pragma unroll 1
-            for (uint32_t h = 0; h < 2; ++h) {
-              if (t >= 2 && !(ok = wait_warp(bar(kBarPVDone + 2 * g + h), (t / 2 - 1) & 1u, abort, status))) return;
+            for (uint32_t i = 0; i < 4; ++i) {
+              const uint32_t h = i >> 1, g = i & 1u, n = g ? done[1] : done[0];
+              if (!(act >> g & 1u)) continue;
+              if (n > 0 && !(ok = wait_warp(bar(kBarPVDone + 2 * g + h), (n - 1) & 1u, abort, status))) return;
               tc_fence_after();
               const uint32_t da = tS0 + g * 128u + h * 64u;
               const uint64_t ka = dK + uint64_t(sg * (L::kTileBytes >> 4)) + uint64_t(h * 512u);  // 64 rows of 128 B
+              const uint64_t qa = dQ + (kPair ? uint64_t(g * (L::kTileBytes >> 4)) : 0u);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) mma_ss_e(da, dQ + kstep(kk), ka + kstep(kk), idS, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) mma_ss_e(da, qa + kstep(kk), ka + kstep(kk), idS, kk > 0 ? 1u : 0u);
               mma_commit_e(bar(kBarSFull + 2 * g + h));
             }
             mma_commit_e(bar(kBarKEmpty + sg));
+            done[0] += act & 1u;
+            done[1] += act >> 1;
             ++kv_it;
           });
           if (!ok) break;
           mma_commit_e(bar(kBarQEmpty));
         }
       } else {
-        while (next_segment()) {
+        while (const volatile ChunkList *list = next_segment()) {
+          const uint32_t both = groups(list->seg);
           uint32_t acc[2] = {0, 0};
           each_chunk([&](int, int) {
-            const uint32_t t = kv_it, g = t & 1u;
-            const int sg = int(t % kStages);
-            if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
+            const uint32_t t = kv_it, act = kPair ? both : 1u << (t & 1u);
+            const int sg = int(t % L::kVStages);
+            if (!(ok = wait_warp(bar(kBarVFull + sg), (t / L::kVStages) & 1u, abort, status))) return;
 #pragma unroll 1
-            for (uint32_t h = 0; h < 2; ++h) {
-              if (!(ok = wait_warp(bar(kBarPFull + 2 * g + h), (t / 2) & 1u, abort, status))) return;
+            for (uint32_t i = 0; i < 4; ++i) {
+              const uint32_t h = i >> 1, g = i & 1u, n = g ? done[1] : done[0];
+              if (!(act >> g & 1u)) continue;
+              if (!(ok = wait_warp(bar(kBarPFull + 2 * g + h), n & 1u, abort, status))) return;
               tc_fence_after();
               // 16 kv rows of P are 8 columns, of V 2 KB
               const uint32_t pa = tS0 + g * 128u + h * 64u, da = tO0 + g * uint32_t(D);
@@ -349,6 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_commit_e(bar(kBarPVDone + 2 * g + h));
             }
             mma_commit_e(bar(kBarVEmpty + sg));
+            done[0] += act & 1u;
+            done[1] += act >> 1;
             ++kv_it;
           });
         }
@@ -367,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tS = tS0 + uint32_t(wg) * 128u + lane_off, tO = tO0 + uint32_t(wg * D) + lane_off;
     float2 *s_ml = reinterpret_cast<float2 *>(smem_raw + L::kMl);
-    uint32_t x_it = 0, seg_n = 0;
+    uint32_t x_it = 0, seg_n = 0, taken = 0;  // taken: chunks of this group
     auto rendezvous = [&]() {  // the warps that hold the same 32 rows (bounded)
       mbar_arrive(bar(kBarXchg + (warp & 3)));
       ok = wait_warp(bar(kBarXchg + (warp & 3)), x_it & 1u, abort, status);
@@ -380,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = g.first, rows = g.rows, t0 = g.t0, h0 = g.hh * p.gg;
       const T *q = static_cast<const T *>(p.q) + g.b * p.q_sb + (int64_t(g.tok0) + t0) * p.q_st;
       constexpr int kPieces = D / 8;  // 16-byte pieces of a row
-      constexpr int kRounds = kTile * kPieces / kSoftmaxThreads;
+      constexpr int kRounds = L::kTile * kPieces / kSoftmaxThreads;
       const int c = tid % kPieces;
       uint4 x[kRounds];
 #pragma unroll
@@ -396,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kRounds; ++i) {
         const int rr = tid / kPieces + i * (kSoftmaxThreads / kPieces);
         // 128-byte swizzle: the 16-byte piece within a row of 128 bytes xor the row
-        *reinterpret_cast<uint4 *>(smem_raw + L::kQ + (c >> 3) * L::kBox + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
+        const int at = kPair ? (rr >> 7) * L::kTileBytes + (rr & 127) * 128 : rr * 128;
+        *reinterpret_cast<uint4 *>(smem_raw + L::kQ + at + (c >> 3) * L::kBox + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kBarQFull));
@@ -406,8 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && list) {
       const volatile SegInfo &g = list->seg;  // read before the list is given back
       const int kvlen = g.kvlen, qbase = kvlen - g.qlen, qb = g.b, slot = g.slot;
-      const bool live = r < g.rows;
-      const int xr = g.first + min(r, g.rows - 1);
+      const int tr = kPair ? wg * kRows + r : r;  // row of the tile
+      const bool live = tr < g.rows, mine = !kPair || wg * kRows < g.rows;
+      const int xr = g.first + min(tr, g.rows - 1);
       const int z = div_gg(p, xr), tq = g.t0 + z, row = g.tok0 + tq, head = g.hh * p.gg + xr - z * p.gg;
       const int64_t *bits = p.tree ? p.tree + qb * p.t_sb + int64_t(row) * p.t_st : nullptr;
       // the columns [u, u + 64) that the row sees
@@ -422,13 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0;  // chunks of this group
       each_chunk([&](const int u0c, int) {
         const uint32_t t = kv_it++;
-        if (int(t & 1u) != wg) return;
+        if (kPair ? !mine : int(t & 1u) != wg) return;
         const int valid_all = kvlen - u0c;
         if (valid_all < 128) {
           // rows past the used length may hold anything: their weights are 0,
           // and their V is made 0 as well before P is published
-          const int sg = int(t % kStages);
-          if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
+          // (pair: both groups write the same zeros, each before its own weights)
+          const int sg = int(t % L::kVStages);
+          if (!(ok = wait_warp(bar(kBarVFull + sg), (t / L::kVStages) & 1u, abort, status))) return;
           uint4 *vt = reinterpret_cast<uint4 *>(smem_raw + L::kV + sg * L::kTileBytes);
           const int per_half = (128 - valid_all) * 8;
           for (int w = r; w < per_half * (D / 64); w += 128) {
@@ -440,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int buf = 2 * wg + h;
-          if (!(ok = wait_warp(bar(kBarSFull + buf), (t / 2) & 1u, abort, status))) return;
+          if (!(ok = wait_warp(bar(kBarSFull + buf), taken & 1u, abort, status))) return;
           tc_fence_after();
           uint32_t x[64];
           tmem_ld_cols<64>(tS + uint32_t(64 * h), x);
@@ -463,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = m_new;
             l *= alpha;
             if (n + h > 0) {  // the products so far must be in O
-              const uint32_t k = t / 2 - (h ? 0u : 1u);  // the group's chunk of the half before this one
+              const uint32_t k = taken - (h ? 0u : 1u);  // the group's chunk of the half before this one
               if (!(ok = wait_warp(bar(kBarPVDone + 2 * wg + (h ^ 1)), k & 1u, abort, status))) return;
               tc_fence_after();
 #pragma unroll 1
@@ -495,67 +519,86 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(bar(kBarPFull + buf));
         }
         ++n;
+        ++taken;
       });
       if (!ok) break;
       // the next segment's Q first: its first scores are computed meanwhile
       list = next_segment();
       if (list) gather_q(list->seg);
       if (!ok) break;
-      // ---- epilogue: the finished rows, or this block's part of them; group
-      // w writes half of the columns from both groups' outputs
-      if (n > 0) {
-        const uint32_t t = kv_it - 1 - uint32_t(int((kv_it - 1) & 1u) != wg);  // this group's last chunk
-        if (!(ok = wait_warp(bar(kBarPVDone + 2 * wg + 1), (t / 2) & 1u, abort, status))) break;
-      }
-      s_ml[wg * 128 + r] = make_float2(m, l);
-      if (!rendezvous()) break;
-      tc_fence_after();
-      const float2 other = s_ml[(wg ^ 1) * 128 + r];
-      const float mx = fmaxf(m, other.x), mref = mx == -INFINITY ? 0.f : mx;
-      const float f_own = ex2(m - mref), f_other = ex2(other.x - mref);
-      const float lsum = l * f_own + other.y * f_other;
-      // a group that saw nothing may have no output at all: its columns are not used
-      const float f0 = wg ? f_other : f_own, f1 = wg ? f_own : f_other;
-      const bool s0 = (wg ? other.x : m) != -INFINITY, s1 = (wg ? m : other.x) != -INFINITY;
-      float o[D / 2];
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        uint32_t a[32], b[32];
-        const uint32_t col = uint32_t(wg * (D / 2) + 32 * h) + lane_off;
-        tmem_ld32(tO0 + col, a);
-        tmem_ld32(tO0 + uint32_t(D) + col, b);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          o[32 * h + c] = (s0 ? __uint_as_float(a[c]) * f0 : 0.f) + (s1 ? __uint_as_float(b[c]) * f1 : 0.f);
-      }
-      tc_fence_before();
-      // the next segment's products write both outputs, and the states' memory is used again
-      if (!rendezvous()) break;
-      if (live) {
+      // ---- epilogue: the finished rows, or this block's part of them
+      if (n > 0 && !(ok = wait_warp(bar(kBarPVDone + 2 * wg + 1), (taken - 1) & 1u, abort, status))) break;
+      // the columns of four from c4 on of this thread's row
+      auto write4 = [&](int c4, float4 o, float mx, float lsum) {
         if (slot < 0) {
           const bool some = lsum > 0.f || lsum != lsum;
           const float inv = some ? 1.f / lsum : 0.f;
-          T *dst = static_cast<T *>(p.out) + qb * p.o_sb + int64_t(row) * p.o_st + int64_t(head) * p.o_sh + wg * (D / 2);
-#pragma unroll
-          for (int c8 = 0; c8 < D / 16; ++c8) {
-            uint4 w;
-            w.x = Pack2<T>::pack(o[8 * c8] * inv, o[8 * c8 + 1] * inv);
-            w.y = Pack2<T>::pack(o[8 * c8 + 2] * inv, o[8 * c8 + 3] * inv);
-            w.z = Pack2<T>::pack(o[8 * c8 + 4] * inv, o[8 * c8 + 5] * inv);
-            w.w = Pack2<T>::pack(o[8 * c8 + 6] * inv, o[8 * c8 + 7] * inv);
-            reinterpret_cast<uint4 *>(dst)[c8] = w;
-          }
-          if (wg == 0 && p.lse)
-            p.lse[qb * p.l_sb + int64_t(row) * p.l_st + int64_t(head) * p.l_sh] =
-                some ? (mx + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+          T *dst = static_cast<T *>(p.out) + qb * p.o_sb + int64_t(row) * p.o_st + int64_t(head) * p.o_sh;
+          reinterpret_cast<uint2 *>(dst)[c4] = make_uint2(Pack2<T>::pack(o.x * inv, o.y * inv), Pack2<T>::pack(o.z * inv, o.w * inv));
         } else {
           // four columns of all rows side by side: a warp's stores are contiguous
-          float4 *dst = reinterpret_cast<float4 *>(p.part_o) + (int64_t(slot) * (D / 4) + wg * (D / 8)) * kTile + r;
+          reinterpret_cast<float4 *>(p.part_o)[(int64_t(slot) * (D / 4) + c4) * L::kTile + tr] = o;
+        }
+      };
+      auto write_state = [&](float mx, float lsum) {
+        if (slot >= 0) {
+          reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * L::kTile + tr] = make_float2(mx, lsum);
+        } else if (p.lse) {
+          p.lse[qb * p.l_sb + int64_t(row) * p.l_st + int64_t(head) * p.l_sh] =
+              lsum > 0.f || lsum != lsum ? (mx + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+        }
+      };
+      if constexpr (kPair) {
+        tc_fence_after();
+        if (mine) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t a[32];
+            tmem_ld32(tO + uint32_t(c), a);
+            tmem_wait_ld();
+            const bool some = m != -INFINITY;  // else there may be no output at all
+            if (live)
 #pragma unroll
-          for (int c4 = 0; c4 < D / 8; ++c4)
-            dst[c4 * kTile] = make_float4(o[4 * c4], o[4 * c4 + 1], o[4 * c4 + 2], o[4 * c4 + 3]);
-          if (wg == 0) reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * kTile + r] = make_float2(mx, lsum);
+              for (int i = 0; i < 8; ++i)
+                write4(c / 4 + i, some ? make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
+                                                     __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f), m, l);
+          }
+          if (live) write_state(m, l);
+        }
+        tc_fence_before();
+      } else {
+        // group w writes half of the columns from both groups' outputs
+        s_ml[wg * kRows + r] = make_float2(m, l);
+        if (!rendezvous()) break;
+        tc_fence_after();
+        const float2 other = s_ml[(wg ^ 1) * kRows + r];
+        const float mx = fmaxf(m, other.x), mref = mx == -INFINITY ? 0.f : mx;
+        const float f_own = ex2(m - mref), f_other = ex2(other.x - mref);
+        const float lsum = l * f_own + other.y * f_other;
+        // a group that saw nothing may have no output at all: its columns are not used
+        const float f0 = wg ? f_other : f_own, f1 = wg ? f_own : f_other;
+        const bool s0 = (wg ? other.x : m) != -INFINITY, s1 = (wg ? m : other.x) != -INFINITY;
+        float o[D / 2];
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t a[32], b[32];
+          const uint32_t col = uint32_t(wg * (D / 2) + 32 * h) + lane_off;
+          tmem_ld32(tO0 + col, a);
+          tmem_ld32(tO0 + uint32_t(D) + col, b);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            o[32 * h + c] = (s0 ? __uint_as_float(a[c]) * f0 : 0.f) + (s1 ? __uint_as_float(b[c]) * f1 : 0.f);
+        }
+        tc_fence_before();
+        // the next segment's products write both outputs, and the states' memory is used again
+        if (!rendezvous()) break;
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            write4(wg * (D / 8) + i, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]), mx, lsum);
+          if (wg == 0) write_state(mx, lsum);
         }
       }
     }
@@ -568,25 +611,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool kPair>
 cudaError_t launch(const DecodeProblem &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
   // at least 120 KB, so that one block (the owner of all TMEM columns) is on an SM
-  const int smem = Layout<D>::kBytes > 120 * 1024 ? Layout<D>::kBytes : 120 * 1024;
-  cudaError_t e = cudaFuncSetAttribute(k_decode_tc<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = Layout<D, kPair>::kBytes > 120 * 1024 ? Layout<D, kPair>::kBytes : 120 * 1024;
+  cudaError_t e = cudaFuncSetAttribute(k_decode_tc<D, BF16, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_dep(k_decode_tc<D, BF16>, dim3(unsigned(p.grid)), dim3(kThreads), size_t(smem), s, p, k, v);
+  return launch_dep(k_decode_tc<D, BF16, kPair>, dim3(unsigned(p.grid)), dim3(kThreads), size_t(smem), s, p, k, v);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_tile(const DecodeProblem &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
+  return p.TR == 2 * kRows ? launch<D, BF16, true>(p, k, v, s) : launch<D, BF16, false>(p, k, v, s);
 }
 
 }  // namespace
 
 void decode_tc_plan(DecodeProblem &p) {
-  p.TR = kTile;
-  p.chunk = kChunk;
-  // as many blocks side by side as a sequence of the mean number of tokens
-  // has tiles (sparse: tiles of one query block, which share an index row)
+  // rows of one head that read the same keys, for a sequence of the mean number
+  // of tokens (sparse: of one query block)
   const int64_t tokens = p.q_layout == BSA_LAYOUT_BNSD ? p.Sq : (p.Tq + p.B - 1) / p.B;
   const int64_t rows = (p.index && tokens > p.BQ ? p.BQ : tokens) * p.gg;
-  const int64_t tiles = (rows + kTile - 1) / kTile;
+  // Above 128 rows a tile of 256: a chunk brought in serves both groups.  With
+  // 128-row tiles the loads of every chunk for each of them, 8.6 TB/s from L2,
+  // were the bound (768 rows over 16384 .. 32768 tokens: kernel 164 us).
+  p.TR = rows > kRows ? 2 * kRows : kRows;
+  p.chunk = kChunk;
+  const int64_t tiles = (rows + p.TR - 1) / p.TR;
   p.group = int32_t(tiles < kMostGroup ? tiles : kMostGroup);
   p.grid = num_sms() / p.group * p.group;
 }
@@ -602,8 +653,8 @@ cudaError_t launch_decode_tc(const DecodeProblem &p, cudaStream_t s) {
   CUtensorMap k, v;
   cudaError_t e = make_kv_maps(t, k, v);
   if (e != cudaSuccess) return e;
-  if (p.dtype == BSA_BF16) return p.D == 64 ? launch<64, true>(p, k, v, s) : launch<128, true>(p, k, v, s);
-  return p.D == 64 ? launch<64, false>(p, k, v, s) : launch<128, false>(p, k, v, s);
+  if (p.dtype == BSA_BF16) return p.D == 64 ? launch_tile<64, true>(p, k, v, s) : launch_tile<128, true>(p, k, v, s);
+  return p.D == 64 ? launch_tile<64, false>(p, k, v, s) : launch_tile<128, false>(p, k, v, s);
 }
 
 }  // namespace bsa
