@@ -4,16 +4,19 @@
 // Math, division of the work and joining of parts: decode.cu, decode_plan.cuh.
 //
 // One block per SM.  TMA loads of 128-token chunks of K and V through
-// three-stage rings (warps 8 and 10); S = Q K^T and O += P V issued by warps 11
-// and 9; two softmax warpgroups that take the chunks in turn, a thread a whole
-// row of 64 scores at a time, each with a running maximum, sum and output of its own.
-// Nothing in the loop passes between the two groups, and while one waits for
-// its products the other has the exponentials to itself; their states are
-// joined at the end of a segment.  A group's 128 columns of S are two buffers of
-// 64, so that its next scores are computed while it works on these.  (Two groups on the column halves of the
-// same chunk, as in the forward pass, met once a chunk: 2640 clocks a chunk
-// against about 1050 of products and 1024 of exponentials.)  TMEM holds four
-// S / P buffers and two outputs: all 512 columns at D = 128.
+// three-stage rings (warps 8 and 10); S = Q K^T issued by warp 11, up to three
+// chunks ahead, O += P V by warp 9; two softmax warpgroups that take the chunks
+// in turn, a thread a whole row of 128 scores.  O is one accumulator, so a row's
+// weights have one reference maximum: the group of a chunk passes it on, as soon
+// as it has it, to the group of the next, which may move it again before its own
+// weights (a move, to a score more than 2^8 above, rescales O and is rare).
+// TMEM: three S / P buffers and O, all 512 columns at D = 128.
+//
+// Measured on the way (kernel, 768 rows over 16384 .. 32768 tokens): two groups
+// on the column halves of one chunk, as in the forward pass, 211 us; an output
+// for each group and two S buffers, whose chain S - softmax - P V - S is 4000
+// clocks long, 164 to 185 us (the products of 64 columns of S take the tensor
+// pipe as long as those of 128).
 //
 // The rows of a tile are gathered (any number of heads and tokens) by the
 // softmax threads, the next segment's before the epilogue of the one before.
@@ -43,9 +46,10 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kRows = 128, kChunk = 128;  // rows of a softmax group, tokens of a chunk
+constexpr int kTile = 128, kChunk = 128;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 256;
+constexpr int kStages = 3;
 constexpr int kKWarp = 8, kPvWarp = 9, kVWarp = 10, kSWarp = 11;
 // a row's reference maximum moves once a score passes it by 2^8: weights stay
 // below 2^8, and the output is rarely rescaled
@@ -75,37 +79,35 @@ enum : int {
   kBarKEmpty = 5,      // + K stage
   kBarVFull = 8,       // + V stage
   kBarVEmpty = 11,     // + V stage
-  kBarSFull = 14,      // + 2 group + half
-  kBarPFull = 18,      // + 2 group + half (one arrival per thread of the group)
-  kBarPVDone = 22,     // + 2 group + half: P V is in O, and the S / P buffer is free
-  kBarXchg = 26,       // + row quarter: rendezvous of the warps on the same 32 rows
-  kBarListFull = 30,   // + list buffer
-  kBarListEmpty = 32,  // + list buffer (one arrival per reading warp)
-  kBarDrain = 34,
-  kBarDrainS = 35,
-  kNumBars = 36
+  kBarSFull = 14,      // + S buffer
+  kBarPFull = 17,      // + S buffer (one arrival per warp of the chunk's group)
+  kBarSFree = 20,      // + S buffer: the product that read its P is done
+  kBarPVDone = 23,     // + chunk & 1
+  kBarODone = 25,      // the segment's products are in O (segments with a chunk)
+  kBarRef = 26,        // + 4 group + row quarter: the reference after the group's chunk is known
+  kBarXchg = 34,       // + row quarter: rendezvous of the warps on the same 32 rows
+  kBarListFull = 38,   // + list buffer
+  kBarListEmpty = 40,  // + list buffer (one arrival per reading warp)
+  kBarDrain = 42,
+  kBarDrainS = 43,
+  kNumBars = 44
 };
 
-// Pair: a tile of 256 rows, a group of 128 each, both of which take every chunk;
-// else a tile of 128 rows, whose chunks the groups take in turn.
-template <int D, bool kPair>
+template <int D>
 struct Layout {
-  static constexpr int kTile = kPair ? 2 * kRows : kRows;
-  // at D = 128 seven 32 KB tiles of Q, K and V fill the shared memory
-  static constexpr int kKStages = 3, kVStages = kPair ? 2 : 3;
   static constexpr int kBox = 128 * 128;  // 128 rows of 64 columns
   static constexpr int kTileBytes = D / 64 * kBox;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + (kPair ? 2 : 1) * kTileBytes;
-  static constexpr int kV = kK + kKStages * kTileBytes;
-  static constexpr int kBars = kV + kVStages * kTileBytes;
-  static constexpr int kMl = kBars + kNumBars * 8;        // [2 groups][128] maximum and sum
-  static constexpr int kLists = kMl + 2 * 128 * 8;        // [2] ChunkList
-  static constexpr int kBlk = kLists + 2 * int(sizeof(ChunkList));  // [32] ids of the walking warp
-  static constexpr int kTmemPtr = kBlk + 64;
+  static constexpr int kK = kQ + kTileBytes;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kBars = kV + kStages * kTileBytes;
+  static constexpr int kRef = kBars + kNumBars * 8;       // [2 groups][128] reference maxima
+  static constexpr int kSum = kRef + 2 * 128 * 4;         // [2 groups][128] sums
+  static constexpr int kLists = kSum + 2 * 128 * 4;       // [2] ChunkList
+  static constexpr int kTmemPtr = kLists + 2 * int(sizeof(ChunkList));
   static constexpr int kAbort = kTmemPtr + 4;
   static constexpr int kBytes = kAbort + 4;
-  static_assert(kMl % 8 == 0 && sizeof(DecScratch<kThreads>) <= 2048, "the plan's scratch");
+  static_assert(kRef % 8 == 0 && sizeof(DecScratch<kThreads>) <= 2048, "the plan's scratch");
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -120,11 +122,11 @@ __device__ __forceinline__ uint64_t tree_bits(const DecodeProblem &p, const int6
 }
 __device__ __forceinline__ uint64_t low_bits(int64_t n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull; }
 
-template <int D, bool BF16, bool kPair>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     k_decode_tc(const DecodeProblem p, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
-  using L = Layout<D, kPair>;
+  using L = Layout<D>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   extern __shared__ unsigned char smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -141,26 +143,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
-    mbar_init(bar(kBarQFull), kSoftmaxThreads);
-    mbar_init(bar(kBarQEmpty), 1);
-    for (int s = 0; s < 3; ++s) {
-      mbar_init(bar(kBarKFull + s), 1);
-      mbar_init(bar(kBarKEmpty + s), 1);
-      mbar_init(bar(kBarVFull + s), 1);
-      mbar_init(bar(kBarVEmpty + s), 1);
+    for (int i = 0; i < kNumBars; ++i) {
+      const bool list_empty = i == kBarListEmpty || i == kBarListEmpty + 1;
+      const bool weights = i >= kBarPFull && i < kBarPFull + 3, xchg = i >= kBarXchg && i < kBarXchg + 4;
+      mbar_init(bar(i), i == kBarQFull ? kSoftmaxThreads : xchg ? 64 : weights ? 4 : list_empty ? kReaders : 1);
     }
-    for (int g = 0; g < 4; ++g) {
-      mbar_init(bar(kBarSFull + g), 1);
-      mbar_init(bar(kBarPFull + g), kRows);
-      mbar_init(bar(kBarPVDone + g), 1);
-    }
-    for (int q = 0; q < 4; ++q) mbar_init(bar(kBarXchg + q), kSoftmaxThreads / 4);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarListFull + i), 1);
-      mbar_init(bar(kBarListEmpty + i), kReaders);
-    }
-    mbar_init(bar(kBarDrain), 1);
-    mbar_init(bar(kBarDrainS), 1);
     *abort = 0;
     fence_barrier_init();
   }
@@ -173,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t len_flags = 0;
   // (the states' memory serves as scratch here; nothing is in static shared
   // memory, so that the tiles start at the aligned window)
-  const DecStart st = dec_start<kThreads>(p, *reinterpret_cast<DecScratch<kThreads> *>(smem_raw + L::kMl), len_flags);
+  const DecStart st = dec_start<kThreads>(p, *reinterpret_cast<DecScratch<kThreads> *>(smem_raw + L::kRef), len_flags);
   if (tid == 0) {
     *status = aligned ? 0u : BSA_FLAG_INTERNAL;
     p.join[blockIdx.x] = DecodeJoin{};
@@ -185,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (len_flags) atomicOr(status, len_flags);
   if (!aligned) return;  // the whole block
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS0 = tmem, tO0 = tmem + 256u;
+  const uint32_t tS0 = tmem, tO0 = tmem + 384u;
 
   uint32_t kv_it = 0, list_it = 0;
   bool ok = true;
@@ -208,17 +195,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
+  // registers: the softmax threads hold a row of 128 scores (256 x 216 + 128 x
+  // 72 = the 384 x 168 of the launch)
   if (warp >= 8) {
+    regs_dec<72>();
     if (warp == kKWarp || warp == kVWarp) {
       // --------------------------------------------------- TMA producers
       const bool is_k = warp == kKWarp;
       const CUtensorMap *map = is_k ? &map_k : &map_v;
       const uint32_t ring = is_k ? sK : sV;
       const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
-      const int stages = is_k ? L::kKStages : L::kVStages;
-      int armed[3] = {-1, -1, -1}, s = 0;
-      uint32_t ph = 0;
+      int armed[kStages] = {-1, -1, -1};
       auto load = [&](int u, int pg, const volatile SegInfo &g) {
+        const int s = int(kv_it % kStages);
+        const uint32_t ph = (kv_it / kStages) & 1u;
         if (!(ok = wait_warp(bar(empty0 + s), ph ^ 1u, abort, status))) return;
         if (lane == 0) {
           int row, last;  // tile coordinates: (0, row, 0, h2, last)
@@ -229,14 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_5d(ring + s * L::kTileBytes, map, bar(full0 + s), 0, row, 0, g.h2, last);
         }
         armed[s] = int(ph);
-        if (++s == stages) s = 0, ph ^= 1u;
+        ++kv_it;
       };
       if (is_k) {
         uint32_t flags = 0;
         DecCursor cursor = cursor_begin(st), here;
         DecBatch d;
         DecSeg seg;
-        uint16_t *blk = reinterpret_cast<uint16_t *>(smem_raw + L::kBlk);
         while (ok && cursor_next(p, st, cursor, d, seg, here)) {
           const DecRows v = dec_rows(p, d, seg.tile);
           const bool whole = seg.cs == 0 && seg.ce == d.chunks;
@@ -252,12 +241,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           DecWalk w = walk_begin(p, here.b, seg.hh, v.irow, here.qoff);
           for (int x = seg.cs & ~31; x < seg.ce && ok; x += 32, ++list_it) {
-            int u, pg;
-            walk_fetch(p, d, here.b, w, x, seg.ce, blk, lane, u, pg);
-            const uint32_t some = __ballot_sync(0xffffffffu, u >= 0 && x + lane >= seg.cs);
-            const int n = __popc(some), i = int(list_it & 1u);
+            const int i = int(list_it & 1u);
             if (!(ok = wait_warp(bar(kBarListEmpty + i), ((list_it >> 1) & 1u) ^ 1u, abort, status))) break;
             volatile ChunkList &list = lists[i];
+            int u, pg;
+            // (the list's own memory serves for the ids)
+            walk_fetch(p, d, here.b, w, x, seg.ce, reinterpret_cast<uint16_t *>(const_cast<int *>(list.u)), lane, u, pg);
+            const uint32_t some = __ballot_sync(0xffffffffu, u >= 0 && x + lane >= seg.cs);
+            const int n = __popc(some);
             if (some >> lane & 1u) {
               const int at = __popc(some & ((1u << lane) - 1u));
               list.u[at] = u;
@@ -295,83 +286,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (*abort && lane == 0) {  // let every copy already issued land before the block exits
-        for (int i = 0; i < 3; ++i)
-          if (armed[i] >= 0) drain_wait(bar(full0 + i), uint32_t(armed[i]));
+        for (int s = 0; s < kStages; ++s)
+          if (armed[s] >= 0) drain_wait(bar(full0 + s), uint32_t(armed[s]));
       }
       __syncwarp();
     } else {
       // ------------------------------------------------------ MMA issuers
-      constexpr uint32_t idS = idesc_f16(BF16, 128, 64, false, false);
+      constexpr uint32_t idS = idesc_f16(BF16, 128, 128, false, false);
       constexpr uint32_t idPV = idesc_f16(BF16, 128, D, false, true);
       const uint64_t dQ = sw128_desc(sQ, 16, 1024);
       const uint64_t dK = sw128_desc(sK, 16, 1024);
       const uint64_t dV = sw128_desc(sV, L::kBox, 1024);
       auto kstep = [](int kk) { return uint64_t((kk >> 2) * (L::kBox >> 4) + (kk & 3) * 2); };
-      // the groups that take the chunk, as bits, and chunks that each has taken
-      uint32_t done[2] = {0, 0};
-      auto groups = [&](const volatile SegInfo &g) { return kPair ? (g.rows > kRows ? 3u : 1u) : 1u << (kv_it & 1u); };
       if (warp == kSWarp) {
-        uint32_t q_it = 0;
-        for (const volatile ChunkList *list; (list = next_segment()) != nullptr; ++q_it) {
-          const uint32_t both = groups(list->seg);
+        for (uint32_t q_it = 0; next_segment(); ++q_it) {
           if (!(ok = wait_warp(bar(kBarQFull), q_it & 1u, abort, status))) break;
           each_chunk([&](int, int) {
-            const uint32_t t = kv_it, act = kPair ? both : 1u << (t & 1u);
-            const int sg = int(t % L::kKStages);
-            if (!(ok = wait_warp(bar(kBarKFull + sg), (t / L::kKStages) & 1u, abort, status))) return;
-#pragma unroll 1
-            for (uint32_t i = 0; i < 4; ++i) {
-              const uint32_t h = i >> 1, g = i & 1u, n = g ? done[1] : done[0];
-              if (!(act >> g & 1u)) continue;
-              if (n > 0 && !(ok = wait_warp(bar(kBarPVDone + 2 * g + h), (n - 1) & 1u, abort, status))) return;
-              tc_fence_after();
-              const uint32_t da = tS0 + g * 128u + h * 64u;
-              const uint64_t ka = dK + uint64_t(sg * (L::kTileBytes >> 4)) + uint64_t(h * 512u);  // 64 rows of 128 B
-              const uint64_t qa = dQ + (kPair ? uint64_t(g * (L::kTileBytes >> 4)) : 0u);
+            const uint32_t t = kv_it, buf = t % 3u;
+            const int sg = int(t % kStages);
+            if (t >= 3 && !(ok = wait_warp(bar(kBarSFree + buf), (t / 3 - 1) & 1u, abort, status))) return;
+            if (!(ok = wait_warp(bar(kBarKFull + sg), (t / kStages) & 1u, abort, status))) return;
+            tc_fence_after();
+            const uint32_t da = tS0 + buf * 128u;
+            const uint64_t ka = dK + uint64_t(sg * (L::kTileBytes >> 4));
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) mma_ss_e(da, qa + kstep(kk), ka + kstep(kk), idS, kk > 0 ? 1u : 0u);
-              mma_commit_e(bar(kBarSFull + 2 * g + h));
-            }
+            for (int kk = 0; kk < D / 16; ++kk) mma_ss_e(da, dQ + kstep(kk), ka + kstep(kk), idS, kk > 0 ? 1u : 0u);
+            mma_commit_e(bar(kBarSFull + buf));
             mma_commit_e(bar(kBarKEmpty + sg));
-            done[0] += act & 1u;
-            done[1] += act >> 1;
             ++kv_it;
           });
           if (!ok) break;
           mma_commit_e(bar(kBarQEmpty));
         }
       } else {
-        while (const volatile ChunkList *list = next_segment()) {
-          const uint32_t both = groups(list->seg);
-          uint32_t acc[2] = {0, 0};
+        while (next_segment()) {
+          uint32_t on = 0;
           each_chunk([&](int, int) {
-            const uint32_t t = kv_it, act = kPair ? both : 1u << (t & 1u);
-            const int sg = int(t % L::kVStages);
-            if (!(ok = wait_warp(bar(kBarVFull + sg), (t / L::kVStages) & 1u, abort, status))) return;
-#pragma unroll 1
-            for (uint32_t i = 0; i < 4; ++i) {
-              const uint32_t h = i >> 1, g = i & 1u, n = g ? done[1] : done[0];
-              if (!(act >> g & 1u)) continue;
-              if (!(ok = wait_warp(bar(kBarPFull + 2 * g + h), n & 1u, abort, status))) return;
-              tc_fence_after();
-              // 16 kv rows of P are 8 columns, of V 2 KB
-              const uint32_t pa = tS0 + g * 128u + h * 64u, da = tO0 + g * uint32_t(D);
-              const uint64_t vd = dV + uint64_t(sg * (L::kTileBytes >> 4)) + uint64_t(h * 512u);
-              uint32_t on = g ? acc[1] : acc[0];
+            const uint32_t t = kv_it, buf = t % 3u;
+            const int sg = int(t % kStages);
+            if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
+            if (!(ok = wait_warp(bar(kBarPFull + buf), (t / 3) & 1u, abort, status))) return;
+            tc_fence_after();
+            const uint32_t pa = tS0 + buf * 128u;  // 16 kv rows of P are 8 columns, of V 2 KB
+            const uint64_t vd = dV + uint64_t(sg * (L::kTileBytes >> 4));
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                mma_ts_e(da, pa + uint32_t(8 * kk), vd + uint64_t(kk * 128), idPV, on);
-                on = 1;
-              }
-              if (g) acc[1] = 1;
-              else acc[0] = 1;
-              mma_commit_e(bar(kBarPVDone + 2 * g + h));
+            for (int kk = 0; kk < 8; ++kk) {
+              mma_ts_e(tO0, pa + uint32_t(8 * kk), vd + uint64_t(kk * 128), idPV, on);
+              on = 1;
             }
+            mma_commit_e(bar(kBarPVDone + int(t & 1u)));
             mma_commit_e(bar(kBarVEmpty + sg));
-            done[0] += act & 1u;
-            done[1] += act >> 1;
+            mma_commit_e(bar(kBarSFree + buf));
             ++kv_it;
           });
+          if (!ok) break;
+          if (on) mma_commit_e(bar(kBarODone));  // (a segment may have no chunk)
         }
       }
       if (*abort) {  // let issued MMAs finish before TMEM is freed
@@ -383,12 +352,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // --------------------------------------------- softmax warpgroups
+    regs_inc<216>();
     const int wg = warp >> 2;
     const int r = tid & 127;  // tile row = TMEM lane
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tS0 + uint32_t(wg) * 128u + lane_off, tO = tO0 + uint32_t(wg * D) + lane_off;
-    float2 *s_ml = reinterpret_cast<float2 *>(smem_raw + L::kMl);
-    uint32_t x_it = 0, seg_n = 0, taken = 0;  // taken: chunks of this group
+    const uint32_t tO = tO0 + lane_off;
+    volatile float *s_ref = reinterpret_cast<volatile float *>(smem_raw + L::kRef);
+    volatile float *s_sum = reinterpret_cast<volatile float *>(smem_raw + L::kSum);
+    const int mine_bar = kBarRef + 4 * wg + (warp & 3), other_bar = kBarRef + 4 * (wg ^ 1) + (warp & 3);
+    uint32_t x_it = 0, seg_n = 0, ended = 0, others = 0;  // others: chunks of the other group so far
     auto rendezvous = [&]() {  // the warps that hold the same 32 rows (bounded)
       mbar_arrive(bar(kBarXchg + (warp & 3)));
       ok = wait_warp(bar(kBarXchg + (warp & 3)), x_it & 1u, abort, status);
@@ -401,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = g.first, rows = g.rows, t0 = g.t0, h0 = g.hh * p.gg;
       const T *q = static_cast<const T *>(p.q) + g.b * p.q_sb + (int64_t(g.tok0) + t0) * p.q_st;
       constexpr int kPieces = D / 8;  // 16-byte pieces of a row
-      constexpr int kRounds = L::kTile * kPieces / kSoftmaxThreads;
+      constexpr int kRounds = kTile * kPieces / kSoftmaxThreads;
       const int c = tid % kPieces;
       uint4 x[kRounds];
 #pragma unroll
@@ -417,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kRounds; ++i) {
         const int rr = tid / kPieces + i * (kSoftmaxThreads / kPieces);
         // 128-byte swizzle: the 16-byte piece within a row of 128 bytes xor the row
-        const int at = kPair ? (rr >> 7) * L::kTileBytes + (rr & 127) * 128 : rr * 128;
-        *reinterpret_cast<uint4 *>(smem_raw + L::kQ + at + (c >> 3) * L::kBox + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
+        *reinterpret_cast<uint4 *>(smem_raw + L::kQ + (c >> 3) * L::kBox + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kBarQFull));
@@ -428,9 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && list) {
       const volatile SegInfo &g = list->seg;  // read before the list is given back
       const int kvlen = g.kvlen, qbase = kvlen - g.qlen, qb = g.b, slot = g.slot;
-      const int tr = kPair ? wg * kRows + r : r;  // row of the tile
-      const bool live = tr < g.rows, mine = !kPair || wg * kRows < g.rows;
-      const int xr = g.first + min(tr, g.rows - 1);
+      const bool live = r < g.rows;
+      const int xr = g.first + min(r, g.rows - 1);
       const int z = div_gg(p, xr), tq = g.t0 + z, row = g.tok0 + tq, head = g.hh * p.gg + xr - z * p.gg;
       const int64_t *bits = p.tree ? p.tree + qb * p.t_sb + int64_t(row) * p.t_st : nullptr;
       // the columns [u, u + 64) that the row sees
@@ -441,164 +411,167 @@ __global__ void __launch_bounds__(kThreads, 1)
         return m;
       };
       const int edge_from = (p.tree || p.causal) ? qbase : kvlen;  // first token that some row may not see
+      // m: the reference after the last chunk that this thread knows of; l: the
+      // sum of this group's weights against it
       float m = -INFINITY, l = 0.f;
-      int n = 0;  // chunks of this group
+      int n = 0;  // chunks of the segment so far
+      // the reference as the other group has left it
+      auto take_reference = [&]() {
+        if (!(ok = wait_warp(bar(other_bar), (others - 1) & 1u, abort, status))) return;
+        if (n > 0) {
+          const float now = s_ref[(wg ^ 1) * 128 + r];
+          if (now != m) {
+            if (l != 0.f) l *= ex2(m - now);
+            m = now;
+          }
+        }
+      };
       each_chunk([&](const int u0c, int) {
-        const uint32_t t = kv_it++;
-        if (kPair ? !mine : int(t & 1u) != wg) return;
+        const uint32_t t = kv_it++, buf = t % 3u;
+        if (int(t & 1u) != wg) {
+          ++others;
+          ++n;
+          return;
+        }
+        if (!(ok = wait_warp(bar(kBarSFull + buf), (t / 3) & 1u, abort, status))) return;
+        tc_fence_after();
+        const uint32_t tS = tS0 + buf * 128u + lane_off;
+        uint32_t x[128];
+        tmem_ld_cols<128>(tS, x);
         const int valid_all = kvlen - u0c;
         if (valid_all < 128) {
           // rows past the used length may hold anything: their weights are 0,
           // and their V is made 0 as well before P is published
-          // (pair: both groups write the same zeros, each before its own weights)
-          const int sg = int(t % L::kVStages);
-          if (!(ok = wait_warp(bar(kBarVFull + sg), (t / L::kVStages) & 1u, abort, status))) return;
+          const int sg = int(t % kStages);
+          if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
           uint4 *vt = reinterpret_cast<uint4 *>(smem_raw + L::kV + sg * L::kTileBytes);
           const int per_half = (128 - valid_all) * 8;
           for (int w = r; w < per_half * (D / 64); w += 128) {
-            const int h = w / per_half, x = w % per_half;
-            vt[h * (L::kBox / 16) + valid_all * 8 + x] = make_uint4(0, 0, 0, 0);
+            const int h = w / per_half, y = w % per_half;
+            vt[h * (L::kBox / 16) + valid_all * 8 + y] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const int buf = 2 * wg + h;
-          if (!(ok = wait_warp(bar(kBarSFull + buf), taken & 1u, abort, status))) return;
-          tc_fence_after();
-          uint32_t x[64];
-          tmem_ld_cols<64>(tS + uint32_t(64 * h), x);
-          tmem_wait_ld();
-          if (u0c + 64 * h + 64 > edge_from) {
+        tmem_wait_ld();
+        if (u0c + kChunk > edge_from) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
             const uint64_t vis = visible(u0c + 64 * h);
             const uint32_t lo = uint32_t(vis), hi = uint32_t(vis >> 32);
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (!((c < 32 ? lo : hi) & (1u << (c & 31)))) x[c] = __float_as_uint(-INFINITY);
+              if (!((c < 32 ? lo : hi) & (1u << (c & 31)))) x[64 * h + c] = __float_as_uint(-INFINITY);
           }
-          float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        }
+        float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 64; ++c) pm[c & 3] = fmaxf(pm[c & 3], __uint_as_float(x[c]));
-          const float cm = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * p.scale_log2;
-          const bool move = cm > m + kSlack;  // (true for a first finite maximum)
-          if (__any_sync(0xffffffffu, move)) {
-            const float m_new = move ? cm : m;
-            const float alpha = move ? ex2(m - m_new) : 1.f;
-            m = m_new;
-            l *= alpha;
-            if (n + h > 0) {  // the products so far must be in O
-              const uint32_t k = taken - (h ? 0u : 1u);  // the group's chunk of the half before this one
-              if (!(ok = wait_warp(bar(kBarPVDone + 2 * wg + (h ^ 1)), k & 1u, abort, status))) return;
-              tc_fence_after();
+        for (int c = 0; c < 128; ++c) pm[c & 3] = fmaxf(pm[c & 3], __uint_as_float(x[c]));
+        const float cm = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * p.scale_log2;
+        if (others > 0) {
+          take_reference();
+          if (!ok) return;
+        }
+        const bool move = cm > m + kSlack;  // (true for a first finite maximum)
+        const float before = m;
+        if (move) m = cm;
+        s_ref[wg * 128 + r] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(mine_bar));
+        if (__any_sync(0xffffffffu, move)) {
+          const float alpha = move ? ex2(before - m) : 1.f;
+          l *= alpha;
+          if (n > 0) {  // every product before must be in O
+            const uint32_t k = t - 1;
+            if (!(ok = wait_warp(bar(kBarPVDone + int(k & 1u)), (k / 2) & 1u, abort, status))) return;
+            tc_fence_after();
 #pragma unroll 1
-              for (int j = 0; j < D / 32; ++j) {
-                uint32_t o[32];
-                tmem_ld32(tO + uint32_t(32 * j), o);
-                tmem_wait_ld();
+            for (int j = 0; j < D / 32; ++j) {
+              uint32_t o[32];
+              tmem_ld32(tO + uint32_t(32 * j), o);
+              tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                tmem_st32(tO + uint32_t(32 * j), o);
-              }
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tmem_st32(tO + uint32_t(32 * j), o);
             }
           }
-          const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: every weight is 0
-          float2 ps[2] = {{0.f, 0.f}, {0.f, 0.f}};
-          const float2 sc = {p.scale_log2, p.scale_log2}, mm = {-ref, -ref};
-          uint32_t pk[32];
+        }
+        const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: every weight is 0
+        float2 ps[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        const float2 sc = {p.scale_log2, p.scale_log2}, mm = {-ref, -ref};
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float2 a = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc, mm);
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 a = fma2(make_float2(__uint_as_float(x[32 * h + c]), __uint_as_float(x[32 * h + c + 1])), sc, mm);
             const float2 e = {ex2(a.x), ex2(a.y)};
             ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], e);
             pk[c >> 1] = Pack2<T>::pack(e.x, e.y);
           }
-          tmem_st32(tS + uint32_t(64 * h), pk);  // over its own S, which is in registers
-          l += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(kBarPFull + buf));
+          tmem_st16(tS + uint32_t(16 * h), pk);  // the whole row of S is in registers
         }
+        l += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPFull + buf));
         ++n;
-        ++taken;
       });
+      if (!ok) break;
+      // the other group's chunk may have been the last
+      if (n > 0 && int((kv_it - 1) & 1u) != wg) take_reference();
       if (!ok) break;
       // the next segment's Q first: its first scores are computed meanwhile
       list = next_segment();
       if (list) gather_q(list->seg);
       if (!ok) break;
-      // ---- epilogue: the finished rows, or this block's part of them
-      if (n > 0 && !(ok = wait_warp(bar(kBarPVDone + 2 * wg + 1), (taken - 1) & 1u, abort, status))) break;
-      // the columns of four from c4 on of this thread's row
-      auto write4 = [&](int c4, float4 o, float mx, float lsum) {
+      // ---- epilogue: the finished rows, or this block's part of them; group
+      // w writes half of the columns from both groups' outputs
+      if (n > 0) {
+        if (!(ok = wait_warp(bar(kBarODone), ended & 1u, abort, status))) break;
+        ++ended;
+      }
+      s_sum[wg * 128 + r] = l;
+      if (!rendezvous()) break;
+      tc_fence_after();
+      const float lsum = s_sum[r] + s_sum[128 + r], mx = m;
+      float o[D / 2];
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t a[32];
+        tmem_ld32(tO + uint32_t(wg * (D / 2) + 32 * h), a);
+        tmem_wait_ld();
+        // (no chunk, or nothing seen: there may be no output at all)
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[32 * h + c] = m != -INFINITY ? __uint_as_float(a[c]) : 0.f;
+      }
+      tc_fence_before();
+      // the next segment's products write O, and the sums' memory is used again
+      if (!rendezvous()) break;
+      if (live) {
         if (slot < 0) {
           const bool some = lsum > 0.f || lsum != lsum;
           const float inv = some ? 1.f / lsum : 0.f;
-          T *dst = static_cast<T *>(p.out) + qb * p.o_sb + int64_t(row) * p.o_st + int64_t(head) * p.o_sh;
-          reinterpret_cast<uint2 *>(dst)[c4] = make_uint2(Pack2<T>::pack(o.x * inv, o.y * inv), Pack2<T>::pack(o.z * inv, o.w * inv));
+          T *dst = static_cast<T *>(p.out) + qb * p.o_sb + int64_t(row) * p.o_st + int64_t(head) * p.o_sh + wg * (D / 2);
+#pragma unroll
+          for (int c8 = 0; c8 < D / 16; ++c8) {
+            uint4 w;
+            w.x = Pack2<T>::pack(o[8 * c8] * inv, o[8 * c8 + 1] * inv);
+            w.y = Pack2<T>::pack(o[8 * c8 + 2] * inv, o[8 * c8 + 3] * inv);
+            w.z = Pack2<T>::pack(o[8 * c8 + 4] * inv, o[8 * c8 + 5] * inv);
+            w.w = Pack2<T>::pack(o[8 * c8 + 6] * inv, o[8 * c8 + 7] * inv);
+            reinterpret_cast<uint4 *>(dst)[c8] = w;
+          }
+          if (wg == 0 && p.lse)
+            p.lse[qb * p.l_sb + int64_t(row) * p.l_st + int64_t(head) * p.l_sh] =
+                some ? (mx + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
         } else {
           // four columns of all rows side by side: a warp's stores are contiguous
-          reinterpret_cast<float4 *>(p.part_o)[(int64_t(slot) * (D / 4) + c4) * L::kTile + tr] = o;
-        }
-      };
-      auto write_state = [&](float mx, float lsum) {
-        if (slot >= 0) {
-          reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * L::kTile + tr] = make_float2(mx, lsum);
-        } else if (p.lse) {
-          p.lse[qb * p.l_sb + int64_t(row) * p.l_st + int64_t(head) * p.l_sh] =
-              lsum > 0.f || lsum != lsum ? (mx + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
-        }
-      };
-      if constexpr (kPair) {
-        tc_fence_after();
-        if (mine) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t a[32];
-            tmem_ld32(tO + uint32_t(c), a);
-            tmem_wait_ld();
-            const bool some = m != -INFINITY;  // else there may be no output at all
-            if (live)
+          float4 *dst = reinterpret_cast<float4 *>(p.part_o) + (int64_t(slot) * (D / 4) + wg * (D / 8)) * kTile + r;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                write4(c / 4 + i, some ? make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
-                                                     __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f), m, l);
-          }
-          if (live) write_state(m, l);
-        }
-        tc_fence_before();
-      } else {
-        // group w writes half of the columns from both groups' outputs
-        s_ml[wg * kRows + r] = make_float2(m, l);
-        if (!rendezvous()) break;
-        tc_fence_after();
-        const float2 other = s_ml[(wg ^ 1) * kRows + r];
-        const float mx = fmaxf(m, other.x), mref = mx == -INFINITY ? 0.f : mx;
-        const float f_own = ex2(m - mref), f_other = ex2(other.x - mref);
-        const float lsum = l * f_own + other.y * f_other;
-        // a group that saw nothing may have no output at all: its columns are not used
-        const float f0 = wg ? f_other : f_own, f1 = wg ? f_own : f_other;
-        const bool s0 = (wg ? other.x : m) != -INFINITY, s1 = (wg ? m : other.x) != -INFINITY;
-        float o[D / 2];
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t a[32], b[32];
-          const uint32_t col = uint32_t(wg * (D / 2) + 32 * h) + lane_off;
-          tmem_ld32(tO0 + col, a);
-          tmem_ld32(tO0 + uint32_t(D) + col, b);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            o[32 * h + c] = (s0 ? __uint_as_float(a[c]) * f0 : 0.f) + (s1 ? __uint_as_float(b[c]) * f1 : 0.f);
-        }
-        tc_fence_before();
-        // the next segment's products write both outputs, and the states' memory is used again
-        if (!rendezvous()) break;
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            write4(wg * (D / 8) + i, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]), mx, lsum);
-          if (wg == 0) write_state(mx, lsum);
+          for (int c4 = 0; c4 < D / 8; ++c4)
+            dst[c4 * kTile] = make_float4(o[4 * c4], o[4 * c4 + 1], o[4 * c4 + 2], o[4 * c4 + 3]);
+          if (wg == 0) reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * kTile + r] = make_float2(mx, lsum);
         }
       }
     }
@@ -611,33 +584,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool BF16, bool kPair>
+template <int D, bool BF16>
 cudaError_t launch(const DecodeProblem &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
   // at least 120 KB, so that one block (the owner of all TMEM columns) is on an SM
-  const int smem = Layout<D, kPair>::kBytes > 120 * 1024 ? Layout<D, kPair>::kBytes : 120 * 1024;
-  cudaError_t e = cudaFuncSetAttribute(k_decode_tc<D, BF16, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = Layout<D>::kBytes > 120 * 1024 ? Layout<D>::kBytes : 120 * 1024;
+  cudaError_t e = cudaFuncSetAttribute(k_decode_tc<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_dep(k_decode_tc<D, BF16, kPair>, dim3(unsigned(p.grid)), dim3(kThreads), size_t(smem), s, p, k, v);
-}
-
-template <int D, bool BF16>
-cudaError_t launch_tile(const DecodeProblem &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
-  return p.TR == 2 * kRows ? launch<D, BF16, true>(p, k, v, s) : launch<D, BF16, false>(p, k, v, s);
+  return launch_dep(k_decode_tc<D, BF16>, dim3(unsigned(p.grid)), dim3(kThreads), size_t(smem), s, p, k, v);
 }
 
 }  // namespace
 
 void decode_tc_plan(DecodeProblem &p) {
-  // rows of one head that read the same keys, for a sequence of the mean number
-  // of tokens (sparse: of one query block)
+  p.TR = kTile;
+  p.chunk = kChunk;
+  // as many blocks side by side as a sequence of the mean number of tokens
+  // has tiles (sparse: tiles of one query block, which share an index row)
   const int64_t tokens = p.q_layout == BSA_LAYOUT_BNSD ? p.Sq : (p.Tq + p.B - 1) / p.B;
   const int64_t rows = (p.index && tokens > p.BQ ? p.BQ : tokens) * p.gg;
-  // Above 128 rows a tile of 256: a chunk brought in serves both groups.  With
-  // 128-row tiles the loads of every chunk for each of them, 8.6 TB/s from L2,
-  // were the bound (768 rows over 16384 .. 32768 tokens: kernel 164 us).
-  p.TR = rows > kRows ? 2 * kRows : kRows;
-  p.chunk = kChunk;
-  const int64_t tiles = (rows + p.TR - 1) / p.TR;
+  const int64_t tiles = (rows + kTile - 1) / kTile;
   p.group = int32_t(tiles < kMostGroup ? tiles : kMostGroup);
   p.grid = num_sms() / p.group * p.group;
 }
@@ -653,8 +618,8 @@ cudaError_t launch_decode_tc(const DecodeProblem &p, cudaStream_t s) {
   CUtensorMap k, v;
   cudaError_t e = make_kv_maps(t, k, v);
   if (e != cudaSuccess) return e;
-  if (p.dtype == BSA_BF16) return p.D == 64 ? launch_tile<64, true>(p, k, v, s) : launch_tile<128, true>(p, k, v, s);
-  return p.D == 64 ? launch_tile<64, false>(p, k, v, s) : launch_tile<128, false>(p, k, v, s);
+  if (p.dtype == BSA_BF16) return p.D == 64 ? launch<64, true>(p, k, v, s) : launch<128, true>(p, k, v, s);
+  return p.D == 64 ? launch<64, false>(p, k, v, s) : launch<128, false>(p, k, v, s);
 }
 
 }  // namespace bsa
