@@ -282,6 +282,10 @@ bsa_status prepare_decode(const bsa_tensor *q, const bsa_tensor *k, const bsa_te
   if ((st = check_values(v, knd, dt)) != BSA_OK) return st;
   if ((st = check_values(out, qnd, dt)) != BSA_OK) return st;
   if (!same_shape(k, v) || !same_shape(q, out) || k->shape[knd - 1] != D) return BSA_ERR_PARAM_INVALID;
+  // the copies of k and v have no form for rows, heads or sequences that share
+  // their memory
+  for (int i = 0; i < knd - 1; ++i)
+    if (k->shape[i] > 1 && (k->stride[i] == 0 || v->stride[i] == 0)) return BSA_ERR_UNSUPPORTED;
   if (!(P.scale >= 0.0) || std::isinf(P.scale)) return BSA_ERR_PARAM_INVALID;
   const int64_t N1 = P.num_heads;
   if ((st = kv_cache(k, cu_kv, seqused, bt, P, B, N2, p.kv)) != BSA_OK) return st;

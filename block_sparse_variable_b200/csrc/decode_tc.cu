@@ -80,17 +80,17 @@ enum : int {
   kBarVFull = 8,       // + V stage
   kBarVEmpty = 11,     // + V stage
   kBarSFull = 14,      // + S buffer
-  kBarPFull = 17,      // + S buffer (one arrival per warp of the chunk's group)
-  kBarSFree = 20,      // + S buffer: the product that read its P is done
-  kBarPVDone = 23,     // + chunk & 1
-  kBarODone = 25,      // the segment's products are in O (segments with a chunk)
-  kBarRef = 26,        // + 4 group + row quarter: the reference after the group's chunk is known
-  kBarXchg = 34,       // + row quarter: rendezvous of the warps on the same 32 rows
-  kBarListFull = 38,   // + list buffer
-  kBarListEmpty = 40,  // + list buffer (one arrival per reading warp)
-  kBarDrain = 42,
-  kBarDrainS = 43,
-  kNumBars = 44
+  kBarPFull = 17,      // + 2 S buffer + half (one arrival per warp of the chunk's group)
+  kBarSFree = 23,      // + S buffer: the product that read its P is done
+  kBarPVDone = 26,     // + chunk & 1
+  kBarODone = 28,      // the segment's products are in O (segments with a chunk)
+  kBarRef = 29,        // + 4 group + row quarter: the reference after the group's chunk is known
+  kBarXchg = 37,       // + row quarter: rendezvous of the warps on the same 32 rows
+  kBarListFull = 41,   // + list buffer
+  kBarListEmpty = 43,  // + list buffer (one arrival per reading warp)
+  kBarDrain = 45,
+  kBarDrainS = 46,
+  kNumBars = 47
 };
 
 template <int D>
@@ -120,6 +120,11 @@ __device__ __forceinline__ uint64_t tree_bits(const DecodeProblem &p, const int6
   const int s = n0 & 63;
   return s ? (word(n0 >> 6) >> s) | (word((n0 >> 6) + 1) << (64 - s)) : word(n0 >> 6);
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint64_t low_bits(int64_t n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull; }
 
 template <int D, bool BF16>
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_v);
     for (int i = 0; i < kNumBars; ++i) {
       const bool list_empty = i == kBarListEmpty || i == kBarListEmpty + 1;
-      const bool weights = i >= kBarPFull && i < kBarPFull + 3, xchg = i >= kBarXchg && i < kBarXchg + 4;
+      const bool weights = i >= kBarPFull && i < kBarPFull + 6, xchg = i >= kBarXchg && i < kBarXchg + 4;
       mbar_init(bar(i), i == kBarQFull ? kSoftmaxThreads : xchg ? 64 : weights ? 4 : list_empty ? kReaders : 1);
     }
     *abort = 0;
@@ -325,14 +330,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t t = kv_it, buf = t % 3u;
             const int sg = int(t % kStages);
             if (!(ok = wait_warp(bar(kBarVFull + sg), (t / kStages) & 1u, abort, status))) return;
-            if (!(ok = wait_warp(bar(kBarPFull + buf), (t / 3) & 1u, abort, status))) return;
-            tc_fence_after();
-            const uint32_t pa = tS0 + buf * 128u;  // 16 kv rows of P are 8 columns, of V 2 KB
-            const uint64_t vd = dV + uint64_t(sg * (L::kTileBytes >> 4));
+#pragma unroll 1
+            for (uint32_t h = 0; h < 2; ++h) {
+              if (!(ok = wait_warp(bar(kBarPFull + 2 * buf + h), (t / 3) & 1u, abort, status))) return;
+              tc_fence_after();
+              const uint32_t pa = tS0 + buf * 128u + h * 32u;  // 16 kv rows of P are 8 columns, of V 2 KB
+              const uint64_t vd = dV + uint64_t(sg * (L::kTileBytes >> 4)) + uint64_t(h * 512u);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              mma_ts_e(tO0, pa + uint32_t(8 * kk), vd + uint64_t(kk * 128), idPV, on);
-              on = 1;
+              for (int kk = 0; kk < 4; ++kk) {
+                mma_ts_e(tO0, pa + uint32_t(8 * kk), vd + uint64_t(kk * 128), idPV, on);
+                on = 1;
+              }
             }
             mma_commit_e(bar(kBarPVDone + int(t & 1u)));
             mma_commit_e(bar(kBarVEmpty + sg));
@@ -465,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; ++c) pm[c & 3] = fmaxf(pm[c & 3], __uint_as_float(x[c]));
+        for (int c = 0; c < 128; c += 2)
+          pm[(c >> 1) & 3] = max3(pm[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
         const float cm = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * p.scale_log2;
         if (others > 0) {
           take_reference();
@@ -509,12 +518,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[c >> 1] = Pack2<T>::pack(e.x, e.y);
           }
           tmem_st16(tS + uint32_t(16 * h), pk);  // the whole row of S is in registers
+          if (h & 1) {  // the products of the first 64 tokens begin half way
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarPFull + 2 * int(buf) + (h >> 1)));
+          }
         }
         l += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPFull + buf));
         ++n;
       });
       if (!ok) break;

@@ -333,7 +333,8 @@ bsa_status bsa_select_blocks(const bsa_tensor *q, const bsa_tensor *means,
  *              words are not seen.
  * mask_type BSA_MASK_CAUSAL is the chain: node j is seen iff j <= t.  A row
  * that sees nothing gets out 0, lse -inf; rows of no sequence are left as they
- * were.  Heads times row tiles times kv chunks of one call stay below 2^32
+ * were.  No stride of k or v is 0 where the extent is above 1
+ * (BSA_ERR_UNSUPPORTED).  Heads times row tiles times kv chunks of one call stay below 2^32
  * (BSA_ERR_UNSUPPORTED above).  Bitwise the same on every run.  Weights are rounded to the inputs'
  * type before their product with V; sums are fp32.  BAD_INDEX as for bsa_fwd;
  * BAD_PAGE is raised for table entries whose tokens a row selects. */

@@ -101,6 +101,8 @@ def test_refusals_decode():
     wide = torch.zeros(s.q.shape[0], s.N1, 132, dtype=s.dtype)[..., :128]          # row stride 132
     assert _code(lambda: ask(q=wide)) == 161002
     n = C.make("BNSD", kvlens=(200, 200), qlens=(70, 70), device="cpu", poison=False)
+    shared = n.k[:1].expand(2, -1, -1, -1)                                         # one cache for two sequences
+    assert _code(lambda: bsa.bsa_decode_get_workspace(n.q, shared, n.v, C.params(n), seqused_kv=n.used)) == 161003
     short = torch.zeros(2, 70, 1, dtype=torch.int64)                               # 64 bits for 70 nodes
     assert _code(lambda: bsa.bsa_decode_get_workspace(n.q, n.k, n.v, C.params(n), tree_mask=short,
                                                       seqused_kv=n.used)) == 161002
