@@ -160,10 +160,13 @@ template <int D, typename T>
 cudaError_t launch(const MeansProblem &p, cudaStream_t s) {
   const int64_t pairs = int64_t(p.kv.B) * p.kv.N2, wide = int64_t(num_sms()) * 8;
   // A whole pass gives every kv block a warp (no barrier, 8 KB of loads in
-  // flight a warp) once there are warps for the whole device; fewer blocks
-  // than that, and an append's, get eight warps each, for their latency.  An
-  // append's thread blocks stride over the kv blocks that there are.
-  if (!p.first_kv && pairs * p.NB >= 4 * wide) {
+  // flight a warp) once there are eight for each SM; fewer blocks than that,
+  // and an append's, get eight warps each, for their latency.  (One against
+  // eight warps, D = 128, blocks of 128 tokens: 512 blocks 8.3 and 6.3 us, 1024
+  // 11 and 10, 2048 14 and 16.5, 32768 159 and 180; blocks of 1024 tokens: 512
+  // 44 and 24, 2048 81 and 83.)  An append's thread blocks stride over the kv
+  // blocks that there are.
+  if (!p.first_kv && pairs * p.NB >= wide) {
     const int64_t grid = 1 + (pairs * p.NB + kThreads / 32 - 1) / (kThreads / 32);
     return launch_dep(k_block_means<D, T, 1>, dim3(unsigned(grid)), dim3(kThreads), 0, s, p, int(p.NB));
   }

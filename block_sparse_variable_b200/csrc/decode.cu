@@ -25,8 +25,11 @@ constexpr int kThreads = 128, kWarps = 4;
 constexpr int kChunk = 64;   // tokens of a step, 16 a warp
 constexpr int kTile = 16;    // query rows of a tile
 constexpr int kStages = 3;
-// query rows of a kv head's group up to which this kernel is taken; above,
-// the tensor core kernel with 128-row tiles
+// Query rows of a kv head's group, in the mean, up to which this kernel is
+// taken; above, the tensor core kernel with 128-row tiles.  (16 sequences of
+// 2048 to 16384 tokens, 8 kv heads: 16 rows 113 us here; 20 rows, two tiles,
+// 202 here and 121 there; 32 rows 206 and 122.  One sequence of 16384 tokens,
+// 20 rows: 37 and 35; of 1500 tokens: 18.6 and 19.7.)
 constexpr int kFewRows = 16;
 
 template <int D>

@@ -41,7 +41,6 @@ namespace bsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFewTokens = 64;  // query rows of an index row, in the mean, for the short path
 constexpr float kStep = 0x1p-24f;  // half a step of fp32, relative
 
 // the additions that an element of a score goes through: 16 products in a chain,
@@ -502,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_scores_few(const SelectProblem 
       float2 acc[4], sq = zero2();
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = zero2();
+#pragma unroll 4
       for (int y = tid / kLanes; y < all; y += kRows) {
         const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + int64_t(y % gg) * p.q_sh + int64_t(y / gg) * p.q_st + col * 8));
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -631,33 +631,33 @@ __global__ void __launch_bounds__(kTileThreads, 4) k_scores_tile(const SelectPro
         float2 sq_a = zero2(), sq_b = zero2();
 #pragma unroll 1
         for (int d0 = 0; d0 < D; d0 += 32) {  // chains of 16 products
-        float2 ta[kMyRows], tb[kMyRows];
+          float2 ta[kMyRows], tb[kMyRows];
 #pragma unroll
-        for (int i = 0; i < kMyRows; ++i) ta[i] = tb[i] = zero2();
+          for (int i = 0; i < kMyRows; ++i) ta[i] = tb[i] = zero2();
 #pragma unroll
-        for (int d = d0; d < d0 + 32; d += 8) {
-          const uint4 xa = *reinterpret_cast<const uint4 *>(ma + d * 2), xb = *reinterpret_cast<const uint4 *>(mb + d * 2);
-          const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+          for (int d = d0; d < d0 + 32; d += 8) {
+            const uint4 xa = *reinterpret_cast<const uint4 *>(ma + d * 2), xb = *reinterpret_cast<const uint4 *>(mb + d * 2);
+            const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            const float2 a0 = Pack2<T>::unpack(wa[c]), a1 = Pack2<T>::unpack(wa[c + 1]);
-            const float2 b0 = Pack2<T>::unpack(wb[c]), b1 = Pack2<T>::unpack(wb[c + 1]);
-            sq_a = fma2(a1, a1, fma2(a0, a0, sq_a));
-            sq_b = fma2(b1, b1, fma2(b0, b0, sq_b));
+            for (int c = 0; c < 4; c += 2) {
+              const float2 a0 = Pack2<T>::unpack(wa[c]), a1 = Pack2<T>::unpack(wa[c + 1]);
+              const float2 b0 = Pack2<T>::unpack(wb[c]), b1 = Pack2<T>::unpack(wb[c + 1]);
+              sq_a = fma2(a1, a1, fma2(a0, a0, sq_a));
+              sq_b = fma2(b1, b1, fma2(b0, b0, sq_b));
 #pragma unroll
-            for (int i = 0; i < kMyRows; ++i) {
-              const float4 q = s_q[row0 + i][d / 4 + c / 2];
-              const float2 q0 = {q.x, q.y}, q1 = {q.z, q.w};
-              ta[i] = fma2(q1, a1, fma2(q0, a0, ta[i]));
-              tb[i] = fma2(q1, b1, fma2(q0, b0, tb[i]));
+              for (int i = 0; i < kMyRows; ++i) {
+                const float4 q = s_q[row0 + i][d / 4 + c / 2];
+                const float2 q0 = {q.x, q.y}, q1 = {q.z, q.w};
+                ta[i] = fma2(q1, a1, fma2(q0, a0, ta[i]));
+                tb[i] = fma2(q1, b1, fma2(q0, b0, tb[i]));
+              }
             }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < kMyRows; ++i) {
-          sa[i] = add2(sa[i], ta[i]);
-          sb[i] = add2(sb[i], tb[i]);
-        }
+          for (int i = 0; i < kMyRows; ++i) {
+            sa[i] = add2(sa[i], ta[i]);
+            sb[i] = add2(sb[i], tb[i]);
+          }
         }
         const int ja = j0 + jt, jb = ja + 64;
 #pragma unroll
@@ -1159,10 +1159,12 @@ template <int D, typename T>
 cudaError_t launch(const SelectProblem &p, cudaStream_t s) {
   const int64_t items = int64_t(p.Rg) * p.Hidx;
   cudaError_t e;
-  // few query rows per index row, in the mean: their sums are a matter of
-  // latency, and an index row has its means to itself
-  const int64_t tokens = p.cu_q ? p.Tq : p.Sq * p.B;
-  if (tokens * (p.N1 / p.Hidx) <= int64_t(p.Rg) * kFewTokens) {
+  // Up to two query blocks per sequence, in the mean: rows hardly share their
+  // block means, so each streams its own, and their sums are a matter of
+  // latency.  (32 sequences of 4096 to 16384 tokens, 32 heads, one 128-token
+  // block: 34 to 41 us against 78 to 119 by tiles; two blocks 46 to 60 against
+  // 65 to 90; three 58 to 79 against 64 to 76; four 70 to 93 against 63 to 79.)
+  if (p.Rg <= 2 * int64_t(p.B)) {
     const int64_t runs = items * (p.NB > 0 ? (p.NB + kFewRun - 1) / kFewRun : 1), wave = int64_t(num_sms()) * 2;
     e = cudaFuncSetAttribute(k_scores_few<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
@@ -1186,8 +1188,10 @@ cudaError_t launch(const SelectProblem &p, cudaStream_t s) {
       if (e != cudaSuccess) return e;
     }
   }
-  // up to 1024 blocks a row's keys fit a warp's registers, and no step of its
-  // search waits for a barrier (a step of a block's took 0.45 us)
+  // Up to 1024 blocks a row's keys fit a warp's registers, and no step of its
+  // search waits for a barrier: the whole call takes 53 us against 71 for 64
+  // single tokens before 1023 blocks, and 86 against 333 for a 32768-token
+  // prompt of 24 heads.  Up to 256, eight registers do: 74 us for that prompt.
   if (p.NB > 1024) return launch_dep(k_choose_wide<D, T>, dim3(unsigned(items)), dim3(kChooseThreads), 0, s, p);
   const dim3 grid(unsigned((items + 3) / 4));
   e = p.NB <= 256 ? launch_dep(k_choose<D, T, 8>, grid, dim3(128), 0, s, p)

@@ -125,6 +125,8 @@ MEANS = [
     dict(layout="TND", kvlens=(333, 0, 1, 2050), BKV=1024, D=64),
     dict(layout="TND", kvlens=(333, 50), dtype=FP, interleaved=True),
     dict(layout="BNSD", kvlens=(260, 0, 384), qlens=(1, 1, 1), N2=3, N1=6),
+    dict(kvlens=(20000, 133, 0), N2=8),                                             # a warp a block
+    dict(layout="TND", kvlens=(40007, 0, 1, 2050), N2=8, BKV=256, D=64, dtype=FP),
 ]
 
 
@@ -189,6 +191,10 @@ SELECT = [
     dict(layout="BNSD", qlens=(2, 2), kvlens=(130000, 9), W=8, N1=2, N2=1, D=64, sink=3, local=3),
     dict(qlens=(1,), kvlens=(600,), W=1),
     dict(qlens=(1, 3), kvlens=(0, 600), W=2, sink=1),
+    dict(qlens=(900, 0, 129, 2, 0), kvlens=(1700, 100, 129, 1500, 9), W=3, rows="query", dtype=FP),
+    dict(layout="TND", qlens=(900, 5), kvlens=(1300, 5), W=4, BKV=256, rows="query", causal=True, sink=2),
+    dict(qlens=(256, 131), kvlens=(1300, 5000), W=4, N1=16, N2=2),                  # 1024 query rows a row
+    dict(qlens=(400,) + (1,) * 9, kvlens=(3000,) + (700,) * 9, W=3, causal=True),   # a prompt among single tokens
 ]
 
 
