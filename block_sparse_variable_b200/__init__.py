@@ -11,6 +11,7 @@ and importing this package fails if the library is missing.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -455,6 +456,14 @@ def _call(name: str, params: Params, tensors, extra, workspace, stream):
     return ws
 
 
+def _on(stream, like):
+    """Context in which the tensors of a call on `stream` are made: filled and
+    later reused in its order."""
+    if stream is None or not like.is_cuda:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=like.device))
+
+
 def _size(name: str, params: Params, tensors, at: int, *extra) -> int:
     """Workspace bytes; the params stand before tensor `at` of the C call."""
     refs = [_ref(describe(t)) for t in tensors]
@@ -482,7 +491,8 @@ def bsa_block_means(k, params: Params, *, cu_seqlens_kv=None, seqused_kv=None, b
             B, most = block_table.shape[0], block_table.shape[1] * k.shape[1]
         else:
             B, most = k.shape[0], k.shape[2]
-        means = torch.zeros(B, N2, -(-most // bkv), k.shape[-1], dtype=k.dtype, device=k.device)
+        with _on(stream, k):
+            means = torch.zeros(B, N2, -(-most // bkv), k.shape[-1], dtype=k.dtype, device=k.device)
     workspace = _call("bsa_block_means", params, (k, cu_seqlens_kv, seqused_kv, block_table, first_kv, means),
                       (0, 0), workspace, stream)
     return means, workspace
@@ -509,14 +519,15 @@ def bsa_select_blocks(q, means, params: Params, *, width=None, index_heads=None,
             raise ValueError("bsa_select_blocks: width or index")
         H = index_heads or params.num_kv_heads or params.num_heads
         bq = params.block_shape[0]
-        if params.q_layout == "BNSD":
-            index = torch.empty(q.shape[0], H, -(-q.shape[2] // bq), width, dtype=torch.uint16, device=q.device)
-        elif rows is not None:
-            index = torch.empty(H, rows, width, dtype=torch.uint16, device=q.device)
-        else:
-            B = cu_seqlens_q.shape[0] - 1
-            most = min(q.shape[0], q.shape[0] // bq + B)
-            index = torch.full((H, most, width), -1, dtype=torch.int16, device=q.device).view(torch.uint16)
+        with _on(stream, q):
+            if params.q_layout == "BNSD":
+                index = torch.empty(q.shape[0], H, -(-q.shape[2] // bq), width, dtype=torch.uint16, device=q.device)
+            elif rows is not None:
+                index = torch.empty(H, rows, width, dtype=torch.uint16, device=q.device)
+            else:
+                B = cu_seqlens_q.shape[0] - 1
+                most = min(q.shape[0], q.shape[0] // bq + B)
+                index = torch.full((H, most, width), -1, dtype=torch.int16, device=q.device).view(torch.uint16)
     workspace = _call("bsa_select_blocks", params, (q, means, cu_seqlens_q, cu_seqlens_kv, seqused_kv, index),
                       (int(sink_blocks), int(local_blocks)), workspace, stream)
     return index, workspace
@@ -538,10 +549,12 @@ def bsa_decode(q, k, v, params: Params, *, index=None, tree_mask=None, cu_seqlen
     """Attention of a few query tokens per sequence over the whole cache or the
     blocks of `index`, with no mask, the causal mask or the ancestor bits of a
     draft tree.  Returns (out, lse, workspace)."""
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None and params.return_lse:
-        lse = q.new_empty(_lse_shape(q, params), dtype=torch.float32)
+    if out is None or lse is None and params.return_lse:
+        with _on(stream, q):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None and params.return_lse:
+                lse = q.new_empty(_lse_shape(q, params), dtype=torch.float32)
     workspace = _call("bsa_decode", params, (q, k, v, index, tree_mask, cu_seqlens_q, cu_seqlens_kv, seqused_kv,
                                              block_table, out, lse), (0, 0), workspace, stream)
     return out, lse, workspace

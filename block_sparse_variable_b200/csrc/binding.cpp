@@ -130,6 +130,12 @@ PyObject *call(PyObject *, PyObject *args) {
       const bsa_status st = query(op, reinterpret_cast<void *>(fn_query), ref, &params, x, &bytes);
       if (st != BSA_OK) return Py_BuildValue("(iOO)", int(st), Py_True, Py_None);
       if (bytes < 256) bytes = 256;
+      // memory of the call's own stream: of another's it could be handed out
+      // again while the kernels run
+      c10::cuda::OptionalCUDAStreamGuard on;
+      if (stream_obj != Py_None)
+        on.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream),
+                                                         static_cast<c10::DeviceIndex>(device)));
       made = at::empty({int64_t(bytes)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, device));
       ws = made.data_ptr();
     } else {

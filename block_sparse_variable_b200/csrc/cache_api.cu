@@ -156,6 +156,12 @@ bsa_status check_ws(uint64_t total, void *ws, size_t bytes) {
 
 uint64_t round256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
+// a call without work: its status word, where there is a workspace, reads 0
+bsa_status finish_empty(void *ws, size_t bytes, void *stream) {
+  if (check_ws(kStWords * 4, ws, bytes) != BSA_OK) return BSA_OK;
+  return cudaMemsetAsync(ws, 0, kStWords * 4, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
 // ------------------------------------------------------------- block means
 bsa_status prepare_means(const bsa_tensor *k, const bsa_tensor *cu_kv, const bsa_tensor *seqused,
                          const bsa_tensor *bt, const bsa_tensor *first, const bsa_params *prm,
@@ -184,7 +190,7 @@ bsa_status prepare_means(const bsa_tensor *k, const bsa_tensor *cu_kv, const bsa
     p.first_kv = static_cast<const int32_t *>(first->data);
   }
   if (B * N2 * (NB > 0 ? NB : 1) >= kMaxGrid) return BSA_ERR_UNSUPPORTED;
-  empty = B == 0 || NB == 0;
+  empty = B == 0;
   p.D = int32_t(D);
   p.NB = int32_t(NB);
   p.dtype = k->dtype;
@@ -229,7 +235,7 @@ bsa_status prepare_select(const bsa_tensor *q, const bsa_tensor *means, const bs
   const int64_t Rg = P.q_layout == BSA_LAYOUT_BNSD ? B * R : R;
   const int64_t chunks = NB > 0 ? cdiv(NB, 128) : 1;
   if (Rg >= kMaxLen || H * Rg * chunks >= kMaxGrid) return BSA_ERR_UNSUPPORTED;
-  empty = B == 0 || Rg == 0;
+  empty = B == 0;
   p.q_layout = P.q_layout;
   p.B = int32_t(B); p.N1 = int32_t(N1); p.N2 = int32_t(N2); p.D = int32_t(D); p.g = int32_t(N1 / N2);
   p.Hidx = int32_t(H); p.BQ = int32_t(P.block_shape[0]); p.BKV = int32_t(P.block_shape[1]);
@@ -371,7 +377,8 @@ bsa_status bsa_block_means(const bsa_tensor *k, const bsa_tensor *cu_kv, const b
   uint64_t bytes;
   bool empty;
   bsa_status st = prepare_means(k, cu_kv, seqused, bt, first_kv, params, means, p, bytes, empty);
-  if (st != BSA_OK || empty) return st;
+  if (st != BSA_OK) return st;
+  if (empty) return finish_empty(workspace, workspace_bytes, stream);
   if ((st = check_ws(bytes, workspace, workspace_bytes)) != BSA_OK) return st;
   p.status = static_cast<uint32_t *>(workspace);
   return launch_block_means(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
@@ -402,7 +409,8 @@ bsa_status bsa_select_blocks(const bsa_tensor *q, const bsa_tensor *means, const
   bool empty;
   bsa_status st = prepare_select(q, means, cu_q, cu_kv, seqused, params, sink_blocks, local_blocks, index, p, L,
                                  bytes, empty);
-  if (st != BSA_OK || empty) return st;
+  if (st != BSA_OK) return st;
+  if (empty) return finish_empty(workspace, workspace_bytes, stream);
   if ((st = check_ws(bytes, workspace, workspace_bytes)) != BSA_OK) return st;
   p.status = at<uint32_t>(workspace, L.status);
   p.row_nk = at<int32_t>(workspace, L.row_nk);
@@ -443,7 +451,8 @@ bsa_status bsa_decode(const bsa_tensor *q, const bsa_tensor *k, const bsa_tensor
   bool empty;
   bsa_status st = prepare_decode(q, k, v, index, tree_mask, cu_q, cu_kv, seqused, bt, params, out, lse, p, L,
                                  bytes, empty);
-  if (st != BSA_OK || empty) return st;
+  if (st != BSA_OK) return st;
+  if (empty) return finish_empty(workspace, workspace_bytes, stream);
   if ((st = check_ws(bytes, workspace, workspace_bytes)) != BSA_OK) return st;
   p.status = at<uint32_t>(workspace, L.status);
   p.flags = at<uint32_t>(workspace, L.flags);

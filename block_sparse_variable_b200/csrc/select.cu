@@ -1188,6 +1188,7 @@ cudaError_t launch(const SelectProblem &p, cudaStream_t s) {
       if (e != cudaSuccess) return e;
     }
   }
+  if (items == 0) return cudaSuccess;  // the lengths have been checked
   // Up to 1024 blocks a row's keys fit a warp's registers, and no step of its
   // search waits for a barrier: the whole call takes 53 us against 71 for 64
   // single tokens before 1023 blocks, and 86 against 333 for a 32768-token

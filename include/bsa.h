@@ -258,7 +258,9 @@ bsa_status bsa_bwd(const bsa_tensor *q, const bsa_tensor *k, const bsa_tensor *v
  * a few query tokens per sequence over the whole cache or the chosen blocks.
  * (Additions of this library; the layouts, descriptors, lengths, block table
  * and status bits are those of the attention passes.)  16-bit q / k / v; D in
- * {64, 128}; fewer than 2^30 tokens stored per sequence or packed tensor.
+ * {64, 128}; fewer than 2^30 tokens stored per sequence or packed tensor.  A
+ * call without sequences or query tokens does nothing but clear the status
+ * word of its workspace, where it is given one.
  *
  * bsa_block_means:
  *     means[b,h,j,:] = (1/n_j) sum of k[b,u,h,:]
@@ -334,10 +336,11 @@ bsa_status bsa_select_blocks(const bsa_tensor *q, const bsa_tensor *means,
  * mask_type BSA_MASK_CAUSAL is the chain: node j is seen iff j <= t.  A row
  * that sees nothing gets out 0, lse -inf; rows of no sequence are left as they
  * were.  No stride of k or v is 0 where the extent is above 1
- * (BSA_ERR_UNSUPPORTED).  Heads times row tiles times kv chunks of one call stay below 2^32
- * (BSA_ERR_UNSUPPORTED above).  Bitwise the same on every run.  Weights are rounded to the inputs'
- * type before their product with V; sums are fp32.  BAD_INDEX as for bsa_fwd;
- * BAD_PAGE is raised for table entries whose tokens a row selects. */
+ * (BSA_ERR_UNSUPPORTED).  Heads times row tiles times kv chunks of one call
+ * stay below 2^32 (BSA_ERR_UNSUPPORTED above).  Bitwise the same on every run.
+ * Weights are rounded to the inputs' type before their product with V; sums
+ * are fp32.  BAD_INDEX as for bsa_fwd; BAD_PAGE is raised for table entries
+ * whose tokens a row selects. */
 bsa_status bsa_decode_get_workspace(const bsa_tensor *q, const bsa_tensor *k, const bsa_tensor *v,
                                     const bsa_tensor *index, const bsa_tensor *tree_mask,
                                     const bsa_tensor *cu_seqlens_q,

@@ -526,3 +526,88 @@ def test_other_stream_and_captured_replay():
         o, l, _ = bsa.bsa_decode(s.q, s.k, s.v, P, index=ix, cu_seqlens_q=s.cu_q, **C.where(s))
         assert torch.equal(ix.view(torch.int16), index.view(torch.int16))
         assert torch.equal(o[:10], out[:10]) and torch.equal(l[:10], lse[:10])
+
+
+@gpu
+def test_made_tensors_are_made_on_the_given_stream():
+    s = C.make(kvlens=(1500, 700), qlens=(300, 1), seed=21)
+    P = C.params(s)
+    m0 = bsa.bsa_block_means(s.k, P, **C.where(s))[0]
+    kw = dict(cu_seqlens_q=s.cu_q, seqused_kv=s.used)
+    i0 = bsa.bsa_select_blocks(s.q, m0, P, width=3, **kw)[0]
+    o0 = bsa.bsa_decode(s.q, s.k, s.v, P, index=i0, block_table=s.table, **kw)[0]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for given in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)  # the current stream is busy: a fill on it comes after the kernels
+        m = bsa.bsa_block_means(s.k, P, **C.where(s), stream=given)[0]
+        i = bsa.bsa_select_blocks(s.q, m, P, width=3, **kw, stream=given)[0]
+        o = bsa.bsa_decode(s.q, s.k, s.v, P, index=i, block_table=s.table, **kw, stream=given)[0]
+        torch.cuda.synchronize()
+        n = sum(s.qlens)  # rows of no sequence are not written
+        assert torch.equal(m, m0) and torch.equal(i.view(torch.int16), i0.view(torch.int16))
+        assert torch.equal(o[:n], o0[:n])
+
+
+@gpu
+def test_empty_calls_report_a_clear_status():
+    s = C.make(kvlens=(300, 5), qlens=(3, 1), poison=False)
+    P, dev = C.params(s), "cuda"
+
+    def dirty():
+        return torch.full((1 << 20,), 255, dtype=torch.uint8, device=dev)
+    none = torch.zeros(1, dtype=torch.int64, device=dev)
+    used = torch.zeros(0, dtype=torch.int32, device=dev)
+    # no sequences
+    m = torch.zeros(0, s.N2, 3, s.D, dtype=s.dtype, device=dev)
+    ws = bsa.bsa_block_means(s.k, P, seqused_kv=used, block_table=s.table[:0], means=m, workspace=dirty())[1]
+    assert bsa.bsa_read_status(ws) == 0
+    ws = bsa.bsa_select_blocks(s.q[:0], m, P, width=2, cu_seqlens_q=none, seqused_kv=used, workspace=dirty())[1]
+    assert bsa.bsa_read_status(ws) == 0
+    ws = bsa.bsa_decode(s.q[:0], s.k, s.v, P, cu_seqlens_q=none, seqused_kv=used, block_table=s.table[:0],
+                        workspace=dirty())[2]
+    assert bsa.bsa_read_status(ws) == 0
+    # sequences without query tokens
+    zero = torch.zeros(s.B + 1, dtype=torch.int64, device=dev)
+    ws = bsa.bsa_decode(s.q[:0], s.k, s.v, P, cu_seqlens_q=zero, seqused_kv=s.used, block_table=s.table,
+                        workspace=dirty())[2]
+    assert bsa.bsa_read_status(ws) == 0
+    # no room for the blocks, no rows for the query blocks
+    m = torch.zeros(s.B, s.N2, 0, s.D, dtype=s.dtype, device=dev)
+    ws = bsa.bsa_block_means(s.k, P, **C.where(s), means=m, workspace=dirty())[1]
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN
+    m = torch.zeros(s.B, s.N2, s.NB, s.D, dtype=s.dtype, device=dev)
+    ws = bsa.bsa_select_blocks(s.q, m, P, width=2, rows=0, cu_seqlens_q=s.cu_q, seqused_kv=s.used,
+                               workspace=dirty())[1]
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_INDEX
+
+
+@gpu
+def test_two_captured_graphs_share_a_workspace():
+    # other lengths, masks and kernels behind the same buffer, replayed in turn
+    a = C.make(kvlens=(3000, 40), qlens=(1, 1), N1=8, N2=2, seed=31)
+    b = C.make(kvlens=(900, 2600), qlens=(40, 17), N1=8, N2=2, seed=32)
+    calls, want = [], []
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    for s, causal in ((a, False), (b, True)):
+        def call(s=s, causal=causal, out=torch.empty_like(s.q), lse=torch.empty(s.q.shape[:2], device="cuda")):
+            return bsa.bsa_decode(s.q, s.k, s.v, C.params(s, causal=causal), cu_seqlens_q=s.cu_q,
+                                  seqused_kv=s.used, block_table=s.table, out=out, lse=lse, workspace=ws)[:2]
+        calls.append(call)
+        want.append([x.clone() for x in call()])
+    graphs, got = [], []
+    for call in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(call())
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1, 0)):
+        for x in got:
+            x[0].zero_(), x[1].zero_()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert bsa.bsa_read_status(ws) == 0
+        for i in (0, 1):
+            valid = slice(0, int((a, b)[i].cu_q[-1]))
+            assert torch.equal(got[i][0][valid], want[i][0][valid]) and torch.equal(got[i][1][valid], want[i][1][valid])
