@@ -34,7 +34,8 @@ struct MeansProblem {
 
 // an index row whose scores are too close for 32 bits
 struct SelectAgain {
-  int32_t r, hi;
+  int32_t r, hi, nk;
+  int32_t b, i;     // sequence, query block within it
   uint32_t lo, up;  // keys between which blocks are scored again
 };
 

@@ -166,12 +166,12 @@ __device__ __forceinline__ const T *q_of(const SelectProblem &p, const Row &row,
 
 // a place in the sequence of steps of k_query_sums: 128 tokens of one head
 struct SumStep {
-  int64_t item;
+  uint32_t item;
   int r, hi, g, t;
   Row row;  // b < 0: past the last query block
 };
 __device__ __forceinline__ int row_tokens(const SelectProblem &p, const Row &w) { return min(p.BQ, w.qlen - w.i * p.BQ); }
-__device__ __forceinline__ bool step_next(const SelectProblem &p, SumStep &s, int64_t end) {  // true: the item is done
+__device__ __forceinline__ bool step_next(const SelectProblem &p, SumStep &s, uint32_t end) {  // true: the item is done
   if ((s.t += 128) < row_tokens(p, s.row)) return false;
   s.t = 0;
   if (++s.g < p.N1 / p.Hidx) return false;
@@ -248,10 +248,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_query_sums(const SelectProblem 
   griddep_launch_next();
   if (blockIdx.x == 0) return check_inputs(p);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = lane % kLanes, sub = lane / kLanes;
-  const int64_t items = int64_t(p.Rg) * p.Hidx, blocks = int64_t(gridDim.x) - 1, c = int64_t(blockIdx.x) - 1;
-  const int64_t lo = items * c / blocks, end = items * (c + 1) / blocks;
+  // (32 bits, which the host has checked: a 64-bit division takes some 500 clocks)
+  const uint32_t items = uint32_t(p.Rg) * uint32_t(p.Hidx), blocks = gridDim.x - 1, c = blockIdx.x - 1;
+  const uint32_t each = items / blocks, extra = items % blocks;
+  const uint32_t lo = c * each + min(c, extra), end = lo + each + (c < extra ? 1u : 0u);
   if (lo >= end) return;
-  SumStep at{lo, int(lo / p.Hidx), int(lo % p.Hidx), 0, 0, {}};
+  SumStep at{lo, int(lo / uint32_t(p.Hidx)), int(lo % uint32_t(p.Hidx)), 0, 0, {}};
   at.row = find_row(p, at.r);
   SumStep ahead = at;
   const uint32_t ring = smem_u32(smem) + uint32_t(warp * S::kStages * S::kStage + lane * 16);
@@ -585,10 +587,9 @@ __global__ void __launch_bounds__(kTileThreads, 4) k_scores_tile(const SelectPro
   __shared__ int s_nk[kTileRows], s_b[kTileRows];
   griddep_wait();
   griddep_launch_next();
-  int64_t id = blockIdx.x;
-  const int j0 = int(id % chunks) * kTileBlocks;
-  id /= chunks;
-  const int hi = int(id % p.Hidx), r0 = int(id / p.Hidx) * kTileRows, tid = threadIdx.x;
+  const uint32_t id = blockIdx.x / uint32_t(chunks);
+  const int j0 = int(blockIdx.x - id * uint32_t(chunks)) * kTileBlocks;
+  const int hi = int(id % uint32_t(p.Hidx)), r0 = int(id / uint32_t(p.Hidx)) * kTileRows, tid = threadIdx.x;
   if (tid < kTileRows) {
     const int nk = r0 + tid < p.Rg ? p.row_nk[r0 + tid] : -1;
     s_nk[tid] = nk;
@@ -724,7 +725,7 @@ __device__ __forceinline__ K nth_key(K least, K most, uint32_t total, uint32_t w
     K mid = lo + (hi - lo) / 2 + 1;
     if (step % 3 != 2) {
       const float a = value(lo), top = __log2f(float(n_lo));
-      const float f = (top - __log2f(float(want))) / (top - __log2f(float(n_hi) + 0.5f));
+      const float f = __fdividef(top - __log2f(float(want)), top - __log2f(float(n_hi) + 0.5f));
       const K at = value.inverse(a + f * (value(hi) - a));
       if (at > lo && at <= hi) mid = at;
     }
@@ -792,16 +793,18 @@ struct ChooseClose {
   bool take[kClose];
 };
 template <int D, typename T>
-__device__ __forceinline__ void choose_again(const SelectProblem &p, int r, int hi, uint32_t lo, uint32_t up) {
+__device__ __forceinline__ void choose_again(const SelectProblem &p, const SelectAgain &a) {
   constexpr int kLanes = D / 8, kRows = kChooseThreads / kLanes, kLoads = 4;
   __shared__ double s_red[kChooseWarps][D], s_q[D];
   __shared__ ChooseClose close;
   __shared__ ChooseRed red;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gg = p.N1 / p.Hidx, nk = p.row_nk[r];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gg = p.N1 / p.Hidx;
+  const int r = a.r, hi = a.hi, nk = a.nk;
+  const uint32_t lo = a.lo, up = a.up;
   uint16_t *out = index_row(p, r, hi);
   const uint32_t first = tid < nk ? uint32_t(p.keys[(int64_t(hi) * p.Rg + r) * p.NB + tid] >> 32) : 0u;
   uint32_t ignore = 0;
-  Row row{p.row_batch[r], p.row_block[r], 0, 0};
+  Row row{a.b, a.i, 0, 0};
   const QBatch qb = q_batch(p.cu_q, p.Sq, p.Tq, row.b, ignore);
   row.qlen = qb.qlen;
   row.q0 = qb.tok0;
@@ -971,23 +974,28 @@ template <int D, typename T>
 __global__ void __launch_bounds__(kChooseThreads) k_choose_again(const SelectProblem p) {
   griddep_wait();
   griddep_launch_next();
+  // (a grid has at most as many blocks as the list has room: the first entry
+  // is read together with their number)
+  SelectAgain a = p.again[blockIdx.x];
   const uint32_t n = *p.again_count;
-  for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
-    const SelectAgain a = p.again[i];
-    choose_again<D, T>(p, a.r, a.hi, a.lo, a.up);
+  for (uint32_t i = blockIdx.x; i < n;) {
+    choose_again<D, T>(p, a);
     __syncthreads();
+    if ((i += gridDim.x) < n) a = p.again[i];
   }
 }
 
 // what a row chooses: false when that needs no scores and is written
 struct Choice {
   uint16_t *out;
-  int nk, sink, local;
+  int nk, b, i, sink, local;
   uint32_t want;  // of the blocks that are not forced
   int64_t row;
 };
 __device__ __forceinline__ bool choice_begin(const SelectProblem &p, int r, int hi, int tid, int threads, Choice &c) {
   c.nk = p.row_nk[r];
+  c.b = p.row_batch[r];
+  c.i = p.row_block[r];
   if (c.nk < 0) return false;
   c.out = index_row(p, r, hi);
   const int W = p.W;
@@ -1028,9 +1036,9 @@ __global__ void __launch_bounds__(128) k_choose(const SelectProblem p) {
   griddep_wait();
   griddep_launch_next();
   const int lane = threadIdx.x & 31;
-  const int64_t id = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (id >= int64_t(p.Rg) * p.Hidx) return;
-  const int hi = int(id % p.Hidx), r = int(id / p.Hidx);
+  const uint32_t id = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (id >= uint32_t(p.Rg) * uint32_t(p.Hidx)) return;
+  const int r = int(id / uint32_t(p.Hidx)), hi = int(id - uint32_t(r) * uint32_t(p.Hidx));
   Choice c;
   if (!choice_begin(p, r, hi, lane, 32, c)) return;
   const uint64_t *keys = p.keys + c.row * p.NB;
@@ -1048,16 +1056,15 @@ __global__ void __launch_bounds__(128) k_choose(const SelectProblem p) {
     const float q = p.qsum[c.row * D + lane + 32 * i];
     q2 = fmaf(q, q, q2);
   }
-  auto each = [&](auto &&f) {
+  auto each = [&](auto &&f) {  // (no threshold is as low as 0)
 #pragma unroll
-    for (int i = 0; i < kKeys; ++i)
-      if (key[i]) f(key[i]);
+    for (int i = 0; i < kKeys; ++i) f(key[i]);
   };
   uint32_t least = ~0u, most = 0, n = 0;
-  each([&](uint32_t k) { least = min(least, k), most = max(most, k), ++n; });
+  each([&](uint32_t k) { least = min(least, k - 1), most = max(most, k), n += k != 0 ? 1u : 0u; });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-  least = __reduce_min_sync(0xffffffffu, least);
+  least = __reduce_min_sync(0xffffffffu, least) + 1;
   most = __reduce_max_sync(0xffffffffu, most);
   big = __reduce_max_sync(0xffffffffu, big);
   auto total = [](uint32_t x) { return __reduce_add_sync(0xffffffffu, x); };
@@ -1072,7 +1079,7 @@ __global__ void __launch_bounds__(128) k_choose(const SelectProblem p) {
   n = 0;
   each([&](uint32_t k) { n += k >= lo ? 1u : 0u; });
   if (!sure || total(n) != c.want) {
-    if (lane == 0) p.again[atomicAdd(p.again_count, 1u)] = {r, hi, lo, up};
+    if (lane == 0) p.again[atomicAdd(p.again_count, 1u)] = {r, hi, c.nk, c.b, c.i, lo, up};
     return;
   }
   int at = 0;
@@ -1147,7 +1154,7 @@ __global__ void __launch_bounds__(kChooseThreads) k_choose_wide(const SelectProb
   const bool sure = close_keys<D>(p, c, tau, q2, __uint_as_float(big), lo, up);
   n = 0;
   each([&](uint32_t k) { n += k >= lo ? 1u : 0u; });
-  if (!sure || total(n) != c.want) return choose_again<D, T>(p, r, hi, lo, up);
+  if (!sure || total(n) != c.want) return choose_again<D, T>(p, {r, hi, c.nk, c.b, c.i, lo, up});
   int at = 0;
   for (int j0 = 0; j0 < c.nk; j0 += kChooseThreads) {
     const int j = j0 + tid;
