@@ -590,22 +590,25 @@ __global__ void __launch_bounds__(kTileThreads, 4) k_scores_tile(const SelectPro
   const uint32_t id = blockIdx.x / uint32_t(chunks);
   const int j0 = int(blockIdx.x - id * uint32_t(chunks)) * kTileBlocks;
   const int hi = int(id % uint32_t(p.Hidx)), r0 = int(id / uint32_t(p.Hidx)) * kTileRows, tid = threadIdx.x;
+  const float4 *qs = reinterpret_cast<const float4 *>(p.qsum + (int64_t(hi) * p.Rg + r0) * D);
+#pragma unroll
+  for (int k = 0; k < kTileRows * (D / 4) / kTileThreads; ++k) {
+    const int i = tid + k * kTileThreads;
+    const bool in = r0 + i / (D / 4) < p.Rg;  // (a row of no query block holds anything: nothing uses it)
+    cp_async16(smem_u32(&s_q[i / (D / 4)][i % (D / 4)]), in ? qs + i : qs, in);
+  }
+  cp_commit();
   if (tid < kTileRows) {
-    const int nk = r0 + tid < p.Rg ? p.row_nk[r0 + tid] : -1;
+    const bool in = r0 + tid < p.Rg;
+    const int nk = in ? p.row_nk[r0 + tid] : -1, b = in ? p.row_batch[r0 + tid] : -1;
     s_nk[tid] = nk;
-    s_b[tid] = nk < 0 ? -1 : p.row_batch[r0 + tid];
+    s_b[tid] = nk < 0 ? -1 : b;
   }
   __syncthreads();
   int most = -1;
 #pragma unroll
   for (int i = 0; i < kTileRows; ++i) most = max(most, s_nk[i]);
-  if (j0 >= most) return;
-  const float4 *qs = reinterpret_cast<const float4 *>(p.qsum + (int64_t(hi) * p.Rg + r0) * D);
-#pragma unroll
-  for (int k = 0; k < kTileRows * (D / 4) / kTileThreads; ++k) {
-    const int i = tid + k * kTileThreads;
-    s_q[i / (D / 4)][i % (D / 4)] = s_nk[i / (D / 4)] >= 0 ? qs[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  if (j0 >= most) return cp_wait<0>();
   const int h2 = hi / (p.Hidx / p.N2), jt = tid & 63, row0 = tid >> 6 << 3;
   for (int first = 0; first < kTileRows;) {
     const int b = s_b[first];
@@ -675,6 +678,7 @@ __global__ void __launch_bounds__(kTileThreads, 4) k_scores_tile(const SelectPro
     }
     first = end;
   }
+  cp_wait<0>();
 }
 
 // ------------------------------------------------------------------- choice
