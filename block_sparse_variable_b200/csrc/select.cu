@@ -1170,23 +1170,25 @@ template <int D, typename T>
 cudaError_t launch(const SelectProblem &p, cudaStream_t s) {
   const int64_t items = int64_t(p.Rg) * p.Hidx;
   cudaError_t e;
+  // two blocks an SM, the first of them for the lengths: one more than that
+  // would begin when another has ended (3 us later here)
+  const int64_t wave = int64_t(num_sms()) * 2 - 1;
   // Up to two query blocks per sequence, in the mean: rows hardly share their
   // block means, so each streams its own, and their sums are a matter of
   // latency.  (32 sequences of 4096 to 16384 tokens, 32 heads, one 128-token
   // block: 34 to 41 us against 78 to 119 by tiles; two blocks 46 to 60 against
   // 65 to 90; three 58 to 79 against 64 to 76; four 70 to 93 against 63 to 79.)
   if (p.Rg <= 2 * int64_t(p.B)) {
-    const int64_t runs = items * (p.NB > 0 ? (p.NB + kFewRun - 1) / kFewRun : 1), wave = int64_t(num_sms()) * 2;
+    const int64_t runs = items * (p.NB > 0 ? (p.NB + kFewRun - 1) / kFewRun : 1);
     e = cudaFuncSetAttribute(k_scores_few<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
     e = launch_dep(k_scores_few<D, T>, dim3(unsigned(1 + (runs < wave ? runs : wave))), dim3(kThreads),
                    FewSmem<D>::kBytes, s, p);
     if (e != cudaSuccess) return e;
   } else {
-    const int64_t blocks = int64_t(num_sms()) * 2;
     e = cudaFuncSetAttribute(k_query_sums<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SumSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    e = launch_dep(k_query_sums<D, T>, dim3(unsigned(1 + (items < blocks ? items : blocks))), dim3(kThreads),
+    e = launch_dep(k_query_sums<D, T>, dim3(unsigned(1 + (items < wave ? items : wave))), dim3(kThreads),
                    SumSmem<D>::kBytes, s, p);
     if (e != cudaSuccess) return e;
     const int chunks = (p.NB + kTileBlocks - 1) / kTileBlocks;
