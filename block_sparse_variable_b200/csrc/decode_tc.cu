@@ -18,8 +18,9 @@
 // clocks long, 164 to 185 us (the products of 64 columns of S take the tensor
 // pipe as long as those of 128).
 //
-// The rows of a tile are gathered (any number of heads and tokens) by the
-// softmax threads, the next segment's before the epilogue of the one before.
+// The rows of a tile are gathered (any number of heads and tokens): the first
+// segment's by the softmax threads, the next one's by the warp that issues the
+// scores, once those of the segment before are done.
 // Only warp 8, which runs ahead, follows the division of the work and walks
 // the index and the block table: it publishes segments and their chunks, 32 at
 // a time, in shared memory.  (Under a loaded memory system a dependent load
@@ -33,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include "cache.h"
+#include "cp_async.cuh"
 #include "decode_plan.cuh"
 #include "f32x2.cuh"
 #include "launch.cuh"
@@ -75,7 +77,7 @@ struct ChunkList {
 };
 
 enum : int {
-  kBarQFull = 0,       // one arrival per softmax thread
+  kBarQFull = 0,       // the first segment's Q: one arrival per softmax thread
   kBarQEmpty = 1,      // the segment's last S has read Q
   kBarKFull = 2,       // + K stage
   kBarKEmpty = 5,      // + K stage
@@ -202,6 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
+  // piece c of row rr of Q: 128-byte swizzle, the 16-byte piece within a row of
+  // 128 bytes xor the row
+  auto swizzled = [](int rr, int c) { return (c >> 3) * L::kBox + rr * 128 + (((c & 7) ^ (rr & 7)) << 4); };
+
   // registers: the softmax threads hold a row of 128 scores (256 x 216 + 128 x
   // 72 = the 384 x 168 of the launch)
   if (warp >= 8) {
@@ -306,8 +312,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dV = sw128_desc(sV, L::kBox, 1024);
       auto kstep = [](int kk) { return uint64_t((kk >> 2) * (L::kBox >> 4) + (kk & 3) * 2); };
       if (warp == kSWarp) {
-        for (uint32_t q_it = 0; next_segment(); ++q_it) {
-          if (!(ok = wait_warp(bar(kBarQFull), q_it & 1u, abort, status))) break;
+        // Q of a segment but the first: while the softmax threads are busy with
+        // the last chunks of the one before, whose products have read its Q
+        auto gather_q = [&](const volatile SegInfo &g) {
+          const int first = g.first, rows = g.rows, h0 = g.hh * p.gg;
+          const T *q = static_cast<const T *>(p.q) + g.b * p.q_sb + (int64_t(g.tok0) + g.t0) * p.q_st;
+          constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+          const int c = lane % kPieces;
+#pragma unroll 4
+          for (int rr = lane / kPieces; rr < kTile; rr += 32 / kPieces) {
+            const int y = first + rr, z = div_gg(p, y);
+            const bool in = rr < rows;
+            cp_async16(sQ + uint32_t(swizzled(rr, c)),
+                       in ? q + int64_t(z) * p.q_st + int64_t(h0 + y - z * p.gg) * p.q_sh + c * 8 : q, in);
+          }
+          cp_commit();
+          cp_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+        };
+        uint32_t q_it = 0;
+        for (; const volatile ChunkList *list = next_segment(); ++q_it) {
+          if (q_it == 0) {
+            if (!(ok = wait_warp(bar(kBarQFull), 0u, abort, status))) break;
+          } else {
+            if (!(ok = wait_warp(bar(kBarQEmpty), (q_it - 1) & 1u, abort, status))) break;
+            gather_q(list->seg);
+          }
           each_chunk([&](int, int) {
             const uint32_t t = kv_it, buf = t % 3u;
             const int sg = int(t % kStages);
@@ -370,19 +401,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile float *s_ref = reinterpret_cast<volatile float *>(smem_raw + L::kRef);
     volatile float *s_sum = reinterpret_cast<volatile float *>(smem_raw + L::kSum);
     const int mine_bar = kBarRef + 4 * wg + (warp & 3), other_bar = kBarRef + 4 * (wg ^ 1) + (warp & 3);
-    uint32_t x_it = 0, seg_n = 0, ended = 0, others = 0;  // others: chunks of the other group so far
+    uint32_t x_it = 0, ended = 0, others = 0;  // others: chunks of the other group so far
     auto rendezvous = [&]() {  // the warps that hold the same 32 rows (bounded)
       mbar_arrive(bar(kBarXchg + (warp & 3)));
       ok = wait_warp(bar(kBarXchg + (warp & 3)), x_it & 1u, abort, status);
       ++x_it;
       return ok;
     };
-    // Q of a segment into shared memory, once the segment before has read its
-    // own; all loads of a thread in flight together
-    auto gather_q = [&](const volatile SegInfo &g) {
-      const int first = g.first, rows = g.rows, t0 = g.t0, h0 = g.hh * p.gg;
-      const T *q = static_cast<const T *>(p.q) + g.b * p.q_sb + (int64_t(g.tok0) + t0) * p.q_st;
-      constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+    const volatile ChunkList *list = next_segment();
+    if (list) {  // the first segment's Q; all loads of a thread in flight together
+      const volatile SegInfo &g = list->seg;
+      const int first = g.first, rows = g.rows, h0 = g.hh * p.gg;
+      const T *q = static_cast<const T *>(p.q) + g.b * p.q_sb + (int64_t(g.tok0) + g.t0) * p.q_st;
+      constexpr int kPieces = D / 8;
       constexpr int kRounds = kTile * kPieces / kSoftmaxThreads;
       const int c = tid % kPieces;
       uint4 x[kRounds];
@@ -393,19 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rr < rows)
           x[i] = __ldg(reinterpret_cast<const uint4 *>(q + int64_t(z) * p.q_st + int64_t(h0 + y - z * p.gg) * p.q_sh) + c);
       }
-      if (!(ok = wait_warp(bar(kBarQEmpty), (seg_n & 1u) ^ 1u, abort, status))) return;
-      ++seg_n;
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int rr = tid / kPieces + i * (kSoftmaxThreads / kPieces);
-        // 128-byte swizzle: the 16-byte piece within a row of 128 bytes xor the row
-        *reinterpret_cast<uint4 *>(smem_raw + L::kQ + (c >> 3) * L::kBox + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x[i];
-      }
+      for (int i = 0; i < kRounds; ++i)
+        *reinterpret_cast<uint4 *>(smem_raw + L::kQ + swizzled(tid / kPieces + i * (kSoftmaxThreads / kPieces), c)) = x[i];
       fence_proxy_async_smem();
       mbar_arrive(bar(kBarQFull));
-    };
-    const volatile ChunkList *list = next_segment();
-    if (list) gather_q(list->seg);
+    }
     while (ok && list) {
       const volatile SegInfo &g = list->seg;  // read before the list is given back
       const int kvlen = g.kvlen, qbase = kvlen - g.qlen, qb = g.b, slot = g.slot;
@@ -534,10 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the other group's chunk may have been the last
       if (n > 0 && int((kv_it - 1) & 1u) != wg) take_reference();
       if (!ok) break;
-      // the next segment's Q first: its first scores are computed meanwhile
-      list = next_segment();
-      if (list) gather_q(list->seg);
-      if (!ok) break;
       // ---- epilogue: the finished rows, or this block's part of them; group
       // w writes half of the columns from both groups' outputs
       if (n > 0) {
@@ -587,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (wg == 0) reinterpret_cast<float2 *>(p.part_ml)[int64_t(slot) * kTile + r] = make_float2(mx, lsum);
         }
       }
+      list = next_segment();
     }
   }
   tc_fence_before();
