@@ -28,8 +28,8 @@ constexpr int kStages = 3;
 // Query rows of a kv head's group, in the mean, up to which this kernel is
 // taken; above, the tensor core kernel with 128-row tiles.  (16 sequences of
 // 2048 to 16384 tokens, 8 kv heads: 16 rows 113 us here; 20 rows, two tiles,
-// 202 here and 121 there; 32 rows 206 and 122.  One sequence of 16384 tokens,
-// 20 rows: 37 and 35; of 1500 tokens: 18.6 and 19.7.)
+// 202 here and 121 there; 32 rows 206 and 120.  One sequence of 16384 tokens,
+// 20 rows: 37 and 35; of 1500 tokens: 18.6 and 19.4.)
 constexpr int kFewRows = 16;
 
 template <int D>

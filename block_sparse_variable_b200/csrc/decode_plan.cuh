@@ -13,9 +13,8 @@
 // Where a head has several row tiles, `group` blocks side by side take the
 // same chunks for as many tiles, at the same time: the keys and values that
 // one of them brings in serve the others from L2 (32 query heads over 4 kv
-// heads; 16 sequences of 4096 to 16384 tokens, 2 tiles: 136 us without groups,
-// 113 to 120 with; 4 of 16384 to 32768, 3 tiles: 110 and 103; 6 tiles: 194 and
-// 168 to 176).
+// heads; 16 sequences of 4096 to 16384 tokens, 2 tiles: 134 us without groups,
+// 107 with; 4 of 16384 to 32768, 3 tiles: 105 and 94; 6 tiles: 179 and 154).
 #pragma once
 
 #include <limits.h>
