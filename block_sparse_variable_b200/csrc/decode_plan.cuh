@@ -20,14 +20,15 @@
 #include <limits.h>
 
 #include "cache.h"
+#include "line.h"
 #include "pack16.cuh"
 
 namespace bsa {
 namespace {
 
-// Positions on the line are unsigned 32-bit numbers (the host refuses sizes
-// that could pass them): a 64-bit division takes some 500 clocks, and several
-// stand between a launch and its first load.
+// Positions on the line are unsigned 32-bit numbers (line.h).  The host refuses
+// sizes that could pass them; sequences that overlap, which the host cannot see,
+// can: such a line is empty, and the call reports BAD_SEQLEN.
 struct DecBatch {
   QBatch q;
   KvBatch kv;
@@ -36,6 +37,7 @@ struct DecBatch {
   int passes;     // turns of a group of blocks over them
   int chunks;     // chunks of a unit
   uint32_t work;  // chunks of all units of the batch
+  uint32_t rows;  // index rows of the batch
 };
 
 __device__ __forceinline__ DecBatch dec_batch(const DecodeProblem &p, int b, uint32_t &flags) {
@@ -53,7 +55,8 @@ __device__ __forceinline__ DecBatch dec_batch(const DecodeProblem &p, int b, uin
     d.chunks = max(1, (d.kv.kvlen + p.chunk - 1) >> p.chunk_sh);
   }
   d.passes = p.group == 1 ? d.tiles : int(unsigned(d.tiles + p.group - 1) / unsigned(p.group));
-  d.work = uint32_t(d.passes) * uint32_t(p.H) * uint32_t(d.chunks);
+  d.work = line_places(uint64_t(uint32_t(d.passes) * uint32_t(p.H)) * uint32_t(d.chunks));
+  d.rows = uint32_t(d.q.qlen + p.BQ - 1) >> p.bq_sh;
   return d;
 }
 
@@ -62,13 +65,13 @@ struct DecStart {
   uint32_t lo, hi;        // this group's range
   uint32_t rem;           // first chunk within batch b
   uint32_t each, extra;   // chunks of a group; the first `extra` groups have one more
-  int b, qoff;            // batch of the first chunk; index rows of the batches before it
+  int b;                  // batch of the first chunk
+  uint32_t qoff;          // index rows of the batches before it
 };
 
 template <int kThreads>
 struct DecScratch {
-  uint32_t work[kThreads / 32];
-  int rows[kThreads / 32];
+  uint32_t work[kThreads / 32], rows[kThreads / 32];
   DecStart start;
 };
 
@@ -78,57 +81,54 @@ __device__ DecStart dec_start(const DecodeProblem &p, DecScratch<kThreads> &sh, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  uint32_t work = 0;
-  int rows = 0;
+  uint32_t work = 0, rows = 0;
   for (int b = b0; b < b1; ++b) {
     const DecBatch d = dec_batch(p, b, flags);
-    work += d.work;
-    rows += (d.q.qlen + p.BQ - 1) >> p.bq_sh;
+    work = line_add(work, d.work);
+    rows = rows_add(rows, d.rows);
   }
-  uint32_t iw = work;
-  int ir = rows;
+  uint32_t iw = work, ir = rows;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, iw, o);
-    const int y = __shfl_up_sync(0xffffffffu, ir, o);
-    if (lane >= o) iw += x, ir += y;
+    const uint32_t x = __shfl_up_sync(0xffffffffu, iw, o), y = __shfl_up_sync(0xffffffffu, ir, o);
+    if (lane >= o) iw = line_add(iw, x), ir = rows_add(ir, y);
   }
+  // (sums that stop cannot be taken apart again: what is before this thread is
+  // what is up to its neighbour)
+  uint32_t bw = __shfl_up_sync(0xffffffffu, iw, 1), br = __shfl_up_sync(0xffffffffu, ir, 1);
+  if (lane == 0) bw = br = 0;
   if (lane == 31) sh.work[warp] = iw, sh.rows[warp] = ir;
   __syncthreads();
-  uint32_t total = 0, bw = iw - work;
-  int br = ir - rows;
+  uint32_t total = 0, wr = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) bw += sh.work[w], br += sh.rows[w];
-    total += sh.work[w];
+    if (w == warp) bw = line_add(total, bw), br = rows_add(wr, br);
+    total = line_add(total, sh.work[w]);
+    wr = rows_add(wr, sh.rows[w]);
   }
-  const uint32_t groups = gridDim.x / unsigned(p.group), c = blockIdx.x / unsigned(p.group);
-  const uint32_t each = total / groups, extra = total % groups;
-  const uint32_t lo = c * each + min(c, extra), hi = lo + each + (c < extra ? 1u : 0u);
-  if (lo < hi) {
-    if (lo >= bw && lo - bw < work) {
+  if (total == kLineOver) {
+    flags |= BSA_FLAG_BAD_SEQLEN;
+    total = 0;
+  }
+  const LinePart part = line_part(total, gridDim.x / unsigned(p.group), blockIdx.x / unsigned(p.group));
+  if (part.lo < part.hi) {
+    if (part.lo >= bw && part.lo - bw < work) {
       uint32_t ignore = 0;
       for (int b = b0; b < b1; ++b) {
         const DecBatch d = dec_batch(p, b, ignore);
-        if (lo - bw < d.work) {
-          sh.start = {lo, hi, lo - bw, each, extra, b, br};
+        if (part.lo - bw < d.work) {
+          sh.start = {part.lo, part.hi, part.lo - bw, part.each, part.extra, b, br};
           break;
         }
         bw += d.work;
-        br += (d.q.qlen + p.BQ - 1) >> p.bq_sh;
+        br = rows_add(br, d.rows);
       }
     }
   } else if (tid == 0) {
-    sh.start = {lo, lo, 0, each, extra, p.B, 0};
+    sh.start = {part.lo, part.lo, 0, part.each, part.extra, p.B, 0};
   }
   __syncthreads();
   return sh.start;
-}
-
-// the group that owns chunk x of the line
-__device__ __forceinline__ uint32_t dec_owner(const DecStart &s, uint32_t x) {
-  const uint32_t big = s.extra * (s.each + 1);  // each >= 1 past it
-  return x < big ? x / (s.each + 1) : s.extra + (x - big) / s.each;
 }
 
 // a block's share of one unit
@@ -176,13 +176,14 @@ struct DecWalk {
   uint32_t flags;
 };
 
-__device__ __forceinline__ DecWalk walk_begin(const DecodeProblem &p, int b, int hh, int irow, int qoff) {
+__device__ __forceinline__ DecWalk walk_begin(const DecodeProblem &p, int b, int hh, int irow, uint32_t qoff) {
   DecWalk w{nullptr, 0, -1, 0, 0};
   if (p.index) {
     // fewer index rows than the lengths need: such a row selects nothing
-    const bool have = p.cu_q ? qoff + irow < p.R : true;
+    const uint32_t row = qoff + uint32_t(irow);  // (both below 2^31)
+    const bool have = p.cu_q ? row < uint32_t(p.R) : true;
     if (!have) { w.slot = p.W; w.flags = BSA_FLAG_BAD_INDEX; }
-    w.row = p.cu_q ? p.index + int64_t(hh) * p.ix_s0 + (have ? int64_t(qoff + irow) * p.ix_s1 : 0)
+    w.row = p.cu_q ? p.index + int64_t(hh) * p.ix_s0 + (have ? int64_t(row) * p.ix_s1 : 0)
                    : p.index + int64_t(b) * p.ix_s0 + int64_t(hh) * p.ix_s1 + int64_t(irow) * p.ix_s2;
   }
   return w;
@@ -250,18 +251,19 @@ __device__ __forceinline__ void walk_fetch(const DecodeProblem &p, const DecBatc
 // A block's place on the line: the segment it is at.
 struct DecCursor {
   uint32_t pos, rem;  // chunk of the line, chunk within the batch
-  int b, qoff;
+  int b;
+  uint32_t qoff;
 };
 __device__ __forceinline__ DecCursor cursor_begin(const DecStart &s) { return {s.lo, s.rem, s.b, s.qoff}; }
 // the segment at the cursor, which is then moved past it; false at the end
 __device__ __forceinline__ bool cursor_next(const DecodeProblem &p, const DecStart &s, DecCursor &c, DecBatch &d,
                                             DecSeg &g, DecCursor &at) {
-  while (c.pos < s.hi && c.b < p.B) {  // (contradictory lengths can end the batches first)
+  while (c.pos < s.hi && c.b < p.B) {
     uint32_t ignore = 0;
     d = dec_batch(p, c.b, ignore);
     if (c.rem >= d.work) {
       c.rem -= d.work;
-      c.qoff += (d.q.qlen + p.BQ - 1) >> p.bq_sh;
+      c.qoff = rows_add(c.qoff, d.rows);
       ++c.b;
       continue;
     }
@@ -283,7 +285,7 @@ __device__ __forceinline__ bool cursor_next(const DecodeProblem &p, const DecSta
 // begins and does not finish.
 __device__ __forceinline__ DecodeJoin dec_join(const DecodeProblem &p, const DecStart &st, const DecCursor &at,
                                                const DecBatch &d, const DecSeg &seg, const DecRows &v, int slot) {
-  const int last = int(dec_owner(st, at.pos + uint32_t(d.chunks - 1)));
+  const int last = int(line_owner(st.each, st.extra, gridDim.x / unsigned(p.group), at.pos + uint32_t(d.chunks - 1)));
   return {d.q.tok0, p.cu_q ? 0 : at.b, seg.hh, v.t0, v.first, v.rows, last - int(blockIdx.x / unsigned(p.group)) + 1, slot};
 }
 

@@ -337,7 +337,9 @@ bsa_status bsa_select_blocks(const bsa_tensor *q, const bsa_tensor *means,
  * that sees nothing gets out 0, lse -inf; rows of no sequence are left as they
  * were.  No stride of k or v is 0 where the extent is above 1
  * (BSA_ERR_UNSUPPORTED).  Heads times row tiles times kv chunks of one call
- * stay below 2^32 (BSA_ERR_UNSUPPORTED above).  Bitwise the same on every run.
+ * stay below 2^32 (BSA_ERR_UNSUPPORTED above); sequences of a decreasing
+ * cu_seqlens_q that overlap and pass that together raise BAD_SEQLEN, and no row
+ * is written.  Bitwise the same on every run.
  * Weights are rounded to the inputs' type before their product with V; sums
  * are fp32.  BAD_INDEX as for bsa_fwd; BAD_PAGE is raised for table entries
  * whose tokens a row selects. */
