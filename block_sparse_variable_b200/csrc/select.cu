@@ -35,6 +35,7 @@
 #include "cp_async.cuh"
 #include "f32x2.cuh"
 #include "launch.cuh"
+#include "line.h"
 #include "pack16.cuh"
 
 namespace bsa {
@@ -82,34 +83,36 @@ __device__ __forceinline__ Row next_row(const SelectProblem &p, Row w, int r) {
   return {-1, 0, 0, 0};
 }
 
-// the batch and query block of global index row r, by the whole block
+// the batch and query block of global index row r, by the whole block (sums of
+// rows stop at a number that no row has: overlapping sequences can have more)
 __device__ Row find_row(const SelectProblem &p, int r) {
-  __shared__ int s_warp[kThreads / 32];
+  __shared__ uint32_t s_warp[kThreads / 32];
   __shared__ Row s_row;
   uint32_t ignore = 0;
   if (!p.cu_q) return {r / p.R, r % p.R, int(p.Sq), 0};
   const int tid = threadIdx.x, lane = tid & 31;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (q_batch(p.cu_q, p.Sq, p.Tq, b, ignore).qlen + p.BQ - 1) / p.BQ;
-  int inc = mine;
+  uint32_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine = rows_add(mine, uint32_t((q_batch(p.cu_q, p.Sq, p.Tq, b, ignore).qlen + p.BQ - 1) / p.BQ));
+  uint32_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
+    const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc = rows_add(inc, x);
   }
+  uint32_t before = __shfl_up_sync(0xffffffffu, inc, 1);
+  if (lane == 0) before = 0;
   if (lane == 31) s_warp[tid >> 5] = inc;
   if (tid == 0) s_row.b = -1;
   __syncthreads();
-  int before = inc - mine;
-  for (int w = 0; w < (tid >> 5); ++w) before += s_warp[w];
-  if (r >= before && r < before + mine) {
+  for (int w = 0; w < (tid >> 5); ++w) before = rows_add(before, s_warp[w]);
+  if (uint32_t(r) >= before && uint32_t(r) - before < mine) {
     for (int b = b0; b < b1; ++b) {
       const QBatch qb = q_batch(p.cu_q, p.Sq, p.Tq, b, ignore);
-      const int nq = (qb.qlen + p.BQ - 1) / p.BQ;
-      if (r < before + nq) {
-        s_row = {b, r - before, qb.qlen, qb.tok0};
+      const uint32_t nq = uint32_t((qb.qlen + p.BQ - 1) / p.BQ);
+      if (uint32_t(r) - before < nq) {
+        s_row = {b, r - int(before), qb.qlen, qb.tok0};
         break;
       }
       before += nq;
@@ -405,8 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_scores_few(const SelectProblem 
   extern __shared__ __align__(128) unsigned char smem[];
   SumRed<D> &red = *reinterpret_cast<SumRed<D> *>(smem + S::kRed);
   float *s_q = reinterpret_cast<float *>(smem + S::kQ);
-  __shared__ uint32_t s_work[kThreads / 32];
-  __shared__ int s_rows[kThreads / 32];
+  __shared__ uint32_t s_work[kThreads / 32], s_rows[kThreads / 32];
   __shared__ FewAt s_at;
   griddep_wait();
   griddep_launch_next();
@@ -415,48 +417,53 @@ __global__ void __launch_bounds__(kThreads, 2) k_scores_few(const SelectProblem 
   {
     const int lane = tid & 31, warp = tid >> 5, per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    uint32_t work = 0;
-    int rows = 0, nq, runs, qlen;
+    uint32_t work = 0, rows = 0;
+    int nq, runs, qlen;
     int64_t tok0;
-    for (int b = b0; b < b1; ++b) {
+    auto places = [&](int b) {  // of the batch's units
       few_batch(p, b, nq, runs, qlen, tok0);
-      work += uint32_t(nq) * uint32_t(p.Hidx) * uint32_t(runs + 1);
-      rows += nq;
+      return line_places(uint64_t(uint32_t(nq) * uint32_t(p.Hidx)) * uint32_t(runs + 1));
+    };
+    for (int b = b0; b < b1; ++b) {
+      work = line_add(work, places(b));
+      rows = rows_add(rows, uint32_t(nq));
     }
-    uint32_t iw = work;
-    int ir = rows;
+    uint32_t iw = work, ir = rows;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, iw, o);
-      const int y = __shfl_up_sync(0xffffffffu, ir, o);
-      if (lane >= o) iw += x, ir += y;
+      const uint32_t x = __shfl_up_sync(0xffffffffu, iw, o), y = __shfl_up_sync(0xffffffffu, ir, o);
+      if (lane >= o) iw = line_add(iw, x), ir = rows_add(ir, y);
     }
+    uint32_t bw = __shfl_up_sync(0xffffffffu, iw, 1), br = __shfl_up_sync(0xffffffffu, ir, 1);
+    if (lane == 0) bw = br = 0;
     if (lane == 31) s_work[warp] = iw, s_rows[warp] = ir;
     if (tid == 0) s_at.left = 0;
     __syncthreads();
-    uint32_t total = 0, bw = iw - work;
-    int br = ir - rows;
+    uint32_t total = 0, wr = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) bw += s_work[w], br += s_rows[w];
-      total += s_work[w];
+      if (w == warp) bw = line_add(total, bw), br = rows_add(wr, br);
+      total = line_add(total, s_work[w]);
+      wr = rows_add(wr, s_rows[w]);
     }
-    const uint32_t blocks = gridDim.x - 1, c = blockIdx.x - 1, each = total / blocks, extra = total % blocks;
-    const uint32_t lo = c * each + min(c, extra), n = each + (c < extra ? 1u : 0u);
+    // The units of the rows that the index has come first: lengths that need
+    // more rows, or overlapping ones that pass 32 bits, lose the others.
+    total = min(total, line_places(uint64_t(uint32_t(p.Rg) * uint32_t(p.Hidx)) * uint32_t((p.NB + kFewRun - 1) / kFewRun + 1)));
+    const LinePart part = line_part(total, gridDim.x - 1, blockIdx.x - 1);
+    const uint32_t lo = part.lo, n = part.hi - part.lo;
     if (n > 0 && lo >= bw && lo - bw < work)
       for (int b = b0; b < b1; ++b) {
-        few_batch(p, b, nq, runs, qlen, tok0);
-        const uint32_t here = uint32_t(nq) * uint32_t(p.Hidx) * uint32_t(runs + 1);
+        const uint32_t here = places(b);
         if (lo - bw < here) {
           const uint32_t unit = (lo - bw) / uint32_t(runs + 1);
-          FewAt a{n, b, br, int(unit / uint32_t(p.Hidx)), int(unit % uint32_t(p.Hidx)),
+          FewAt a{n, b, int(br), int(unit / uint32_t(p.Hidx)), int(unit % uint32_t(p.Hidx)),
                   int((lo - bw) % uint32_t(runs + 1)), nq, runs, qlen, tok0, 0};
           if (a.r0 + a.i < p.Rg) a.nk = candidates(p, few_row(a));
           s_at = a;
           break;
         }
         bw += here;
-        br += nq;
+        br = rows_add(br, uint32_t(nq));
       }
     __syncthreads();
   }

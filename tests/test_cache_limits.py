@@ -9,7 +9,7 @@ import torch
 
 import block_sparse_variable_b200 as bsa
 from tests import cache_cases as C
-from tests.test_cache_ops import _decode
+from tests.test_cache_ops import _as_rows, _decode, _select
 
 gpu = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -67,3 +67,54 @@ def test_decode_overlapping_sequences_past_the_line(N1, pages):
     _, _, ws = bsa.bsa_decode(q, k, k.clone(), P, cu_seqlens_q=cu, seqused_kv=used, block_table=table, out=out, lse=lse)
     assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN
     assert (out == 3).all() and (lse == 3).all()
+
+
+@gpu
+@pytest.mark.parametrize("T", [4, 500])  # rows that stream their own means, tiles
+def test_select_overlapping_sequences(T):
+    """Index rows belong to one sequence each, also where query tokens do not."""
+    s = C.make(kvlens=(2000, 300, 1500), qlens=(T, 0, T + 1), N1=4, tail_rows=0, seed=18)
+    s.qd[2][:2] = s.qd[0][-2:]
+    s.q = torch.cat([s.qd[0], s.qd[2][2:]]).cuda()
+    s.cu_q = torch.tensor([0, T, T - 2, 2 * T - 1], device="cuda")
+    means = torch.randn(s.B, s.N2, s.NB, s.D, generator=s.g).to(s.dtype).cuda()
+    index, ws = _select(s, means, dict(W=3))
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN
+    assert torch.equal(_as_rows(s, index), C.ref_select(s, means, 3, "group").int())
+
+
+@gpu
+def test_select_overlapping_sequences_past_the_line():
+    """128 sequences of all query tokens: 2^32 places for the rows that they
+    need, of which the index has four."""
+    T, N1, D, NB, W = 1 << 18, 32, 64, 65408, 5
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(1, N1, D, generator=g).to(BF).cuda().expand(T, N1, D)
+    cu = torch.tensor([0, T] * 128, device="cuda")
+    B = cu.shape[0] - 1
+    means = torch.randn(1, 1, NB, D, generator=g).to(BF).cuda().expand(B, 1, NB, D)
+    used = torch.full((B,), NB * 128, dtype=torch.int32, device="cuda")
+    P = bsa.params_for("TND", "PA_BBND", N1, 1)
+    index = torch.full((N1, 4, W), 77, dtype=torch.int16, device="cuda").view(torch.uint16)
+    _, ws = bsa.bsa_select_blocks(q, means, P, cu_seqlens_q=cu, seqused_kv=used, index=index)
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN | bsa.FLAG_BAD_INDEX
+    best = (q[0].double() @ means[0, 0].double().T).topk(W, dim=1).indices.sort(dim=1).values
+    assert torch.equal((index.to(torch.int32) & 0xFFFF), best.int().unsqueeze(1).expand(-1, 4, -1))
+
+
+@gpu
+def test_select_overlapping_sequences_past_32_bit_rows():
+    """600 sequences of 2^30 - 128 query tokens (one row of memory): more than
+    2^32 index rows, of which there are 2500, all of the first sequence."""
+    T, D = (1 << 30) - 128, 64
+    q = torch.ones(1, 1, D, dtype=BF, device="cuda").expand(T, 1, D)
+    cu = torch.tensor([0, T] * 600, device="cuda")
+    B = cu.shape[0] - 1
+    means = torch.stack([torch.zeros(D), torch.ones(D)]).to(BF).cuda().expand(B, 1, 2, D)
+    used = torch.full((B,), 128, dtype=torch.int32, device="cuda")
+    used[0] = 256  # the other sequences have block 0 alone
+    P = bsa.params_for("TND", "PA_BBND", 1, 1)
+    index = torch.full((1, 2500, 1), 77, dtype=torch.int16, device="cuda").view(torch.uint16)
+    _, ws = bsa.bsa_select_blocks(q, means, P, cu_seqlens_q=cu, seqused_kv=used, index=index)
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN | bsa.FLAG_BAD_INDEX
+    assert (index.to(torch.int32) == 1).all()
