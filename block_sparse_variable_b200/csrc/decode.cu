@@ -509,11 +509,12 @@ bool decode_plan(DecodeProblem &p) {
   p.bkv_sh = log2(p.kv.BKV);
   p.tpb = int32_t((int64_t(p.BQ) * p.gg + p.TR - 1) >> p.tr_sh);
   p.gg_inv = p.gg == 1 ? 0u : uint32_t(((int64_t(1) << 32) + p.gg - 1) / p.gg);
-  // chunks of all units, at most
+  // chunks of all units, at most: as dec_batch counts them, for the longest cache
   const int64_t all = p.q_layout == BSA_LAYOUT_BNSD ? p.Sq * p.B : p.Tq;
   const int64_t tiles = ((all * p.gg) >> p.tr_sh) + (p.index ? (all >> p.bq_sh) + p.B : p.B) + int64_t(p.group) * p.B;
-  const int64_t kv = p.kv.layout == BSA_LAYOUT_TND ? p.kv.Tkv : p.kv.Skv;
-  const int64_t chunks = ((kv + p.chunk - 1) >> p.chunk_sh) + 1;
+  const int64_t kv = p.kv.layout == BSA_LAYOUT_TND ? p.kv.Tkv : p.kv.Skv, nk = (kv + p.kv.BKV - 1) >> p.bkv_sh;
+  const int64_t some = p.index ? (p.W < nk ? p.W : nk) << (p.bkv_sh - p.chunk_sh) : (kv + p.chunk - 1) >> p.chunk_sh;
+  const int64_t chunks = some > 0 ? some : 1;
   return p.gg < 65536 - 256 && double(tiles) * double(p.H) * double(chunks) < 4.0e9;
 }
 

@@ -1,5 +1,6 @@
 """The cache operators at the ends of what they accept: lengths that contradict
 the storage, sizes near the limits, rules that switch kernels."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -27,6 +28,27 @@ def test_line_arithmetic(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr
     assert r.stdout.strip() == "ok"
+
+
+def _decode_shapes(T, B, N1, N2, pages, BKV, W):
+    """Status of bsa_decode_get_workspace for a paged call of these sizes (no memory behind it)."""
+    d = {"q": ((T, N1, 64), BF), "k": ((1, 128, N2, 64), BF), "v": ((1, 128, N2, 64), BF),
+         "index": None if W is None else ((N2, B, W), torch.uint16), "tree": None, "cu_q": ((B + 1,), torch.int64),
+         "cu_kv": None, "used": ((B,), torch.int32), "table": ((B, pages), torch.int32), "out": ((T, N1, 64), BF),
+         "lse": ((T, N1), torch.float32)}
+    d = [None if x is None else bsa.describe_shape(*x) for x in d.values()]
+    refs = [None if x is None else ctypes.byref(x) for x in d]
+    prm, n = bsa.params_for("TND", "PA_BBND", N1, N2, (128, BKV)).c(), ctypes.c_size_t(0)
+    return bsa.lib().bsa_decode_get_workspace(*refs[:9], ctypes.byref(prm), *refs[9:], ctypes.byref(n))
+
+
+def test_decode_refuses_more_chunks_than_the_line_counts():
+    """280 million single tokens before up to 128 tokens: 2 chunks a sequence of
+    the whole cache or of one selected block of 128 tokens, 16 of a block of 1024."""
+    n = 280_000_000
+    assert _decode_shapes(n, n, 1, 1, 1, 1024, None) == 0
+    assert _decode_shapes(n, n, 1, 1, 1, 128, 1) == 0
+    assert _decode_shapes(n, n, 1, 1, 1, 1024, 1) == 161003
 
 
 # ------------------------------------------------- sequences that overlap
