@@ -37,8 +37,12 @@ inline bool same_shape(const bsa_tensor *a, const bsa_tensor *b) {
   return true;
 }
 
+// whole numbers start at a multiple of their size: a load from elsewhere faults
+inline bool aligned_to(const bsa_tensor *t, unsigned bytes) { return reinterpret_cast<uintptr_t>(t->data) % bytes == 0; }
+
 inline bool vec_ok(const bsa_tensor *t, int dtype, int64_t n) {
-  return t->ndim == 1 && t->dtype == dtype && t->shape[0] == n && (n <= 1 || t->stride[0] == 1);
+  return t->ndim == 1 && t->dtype == dtype && t->shape[0] == n && (n <= 1 || t->stride[0] == 1) &&
+         aligned_to(t, dtype == BSA_I64 ? 8 : 4);
 }
 
 inline uint64_t place(uint64_t &cur, uint64_t bytes, bsa_ws_region &r) {

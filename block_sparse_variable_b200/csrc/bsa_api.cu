@@ -29,6 +29,7 @@ int num_sms() {
 
 namespace {
 
+using bsa::aligned_to;
 using bsa::at;
 using bsa::block_ok;
 using bsa::cdiv;
@@ -134,7 +135,7 @@ bsa_status prepare(const Args &a, Problem &p, Layout &L, bool &empty) {
       if (a.k->shape[2] != N2) return BSA_ERR_PARAM_INVALID;
       if (page <= 0 || page % 128 != 0) return BSA_ERR_UNSUPPORTED;
       if (a.bt->ndim != 2 || a.bt->dtype != BSA_I32 || a.bt->shape[0] != B ||
-          a.bt->shape[1] < 1 || (a.bt->shape[1] > 1 && a.bt->stride[1] != 1))
+          a.bt->shape[1] < 1 || (a.bt->shape[1] > 1 && a.bt->stride[1] != 1) || !aligned_to(a.bt, 4))
         return BSA_ERR_PARAM_INVALID;
       max_pages = a.bt->shape[1];
     }
@@ -144,7 +145,7 @@ bsa_status prepare(const Args &a, Problem &p, Layout &L, bool &empty) {
   // index
   const bsa_tensor *ix = a.index;
   int64_t Hidx = 0, R = 0, W = 0;
-  if (ix->dtype != BSA_U16) return BSA_ERR_PARAM_INVALID;
+  if (ix->dtype != BSA_U16 || !aligned_to(ix, 2)) return BSA_ERR_PARAM_INVALID;
   if (ql == BSA_LAYOUT_BNSD) {
     if (ix->ndim != 4 || ix->shape[0] != B || ix->shape[2] != cdiv(Sq, BQ))
       return BSA_ERR_PARAM_INVALID;

@@ -72,7 +72,7 @@ bsa_status kv_cache(const bsa_tensor *k, const bsa_tensor *cu_kv, const bsa_tens
     const int64_t page = k->shape[1];
     if (page <= 0 || page % 128 != 0) return BSA_ERR_UNSUPPORTED;
     if (bt->ndim != 2 || bt->dtype != BSA_I32 || bt->shape[0] != B || bt->shape[1] < 1 ||
-        (bt->shape[1] > 1 && bt->stride[1] != 1) || bt->stride[0] < 0)
+        (bt->shape[1] > 1 && bt->stride[1] != 1) || bt->stride[0] < 0 || !aligned_to(bt, 4))
       return BSA_ERR_PARAM_INVALID;
     if (k->shape[0] >= kMaxLen || page >= kMaxLen || bt->shape[1] >= kMaxLen / page) return BSA_ERR_UNSUPPORTED;
     kv.page_size = int32_t(page);
@@ -131,7 +131,7 @@ bsa_status check_q(const bsa_tensor *q, const bsa_tensor *cu_q, const bsa_params
 // (BNSD) or in all (TND), and width
 bsa_status check_index(const bsa_tensor *ix, const bsa_params &P, int64_t B, int64_t Sq, int64_t N1, int64_t N2,
                        int64_t &H, int64_t &R, int64_t &W) {
-  if (ix->dtype != BSA_U16) return BSA_ERR_PARAM_INVALID;
+  if (ix->dtype != BSA_U16 || !aligned_to(ix, 2)) return BSA_ERR_PARAM_INVALID;
   if (P.q_layout == BSA_LAYOUT_BNSD) {
     if (ix->ndim != 4 || ix->shape[0] != B || ix->shape[2] != cdiv(Sq, P.block_shape[0]))
       return BSA_ERR_PARAM_INVALID;
@@ -305,7 +305,7 @@ bsa_status prepare_decode(const bsa_tensor *q, const bsa_tensor *k, const bsa_te
     if (P.mask_type != BSA_MASK_NONE) return BSA_ERR_PARAM_INVALID;  // the bits are the whole mask
     const int n = qnd - 1;  // the tokens of q, then the words
     if (tree->dtype != BSA_I64 || tree->ndim != n || tree->shape[n - 1] < 1 || tree->shape[n - 1] >= kMaxLen / 64 ||
-        (tree->shape[n - 1] > 1 && tree->stride[n - 1] != 1) || reinterpret_cast<uintptr_t>(tree->data) % 8 != 0)
+        (tree->shape[n - 1] > 1 && tree->stride[n - 1] != 1) || !aligned_to(tree, 8))
       return BSA_ERR_PARAM_INVALID;
     if (P.q_layout == BSA_LAYOUT_BNSD) {
       if (tree->shape[0] != B || tree->shape[1] != Sq || tree->shape[2] * 64 < Sq) return BSA_ERR_PARAM_INVALID;
@@ -320,7 +320,7 @@ bsa_status prepare_decode(const bsa_tensor *q, const bsa_tensor *k, const bsa_te
   }
   if (P.return_lse) {
     if (!present(lse)) return BSA_ERR_NULLPTR;
-    if (lse->dtype != BSA_F32 || lse->ndim != qnd - 1 || reinterpret_cast<uintptr_t>(lse->data) % 4 != 0)
+    if (lse->dtype != BSA_F32 || lse->ndim != qnd - 1 || !aligned_to(lse, 4))
       return BSA_ERR_PARAM_INVALID;
     for (int i = 0; i < qnd - 1; ++i)
       if (lse->shape[i] != q->shape[i] || lse->stride[i] < 0) return BSA_ERR_PARAM_INVALID;

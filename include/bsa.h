@@ -76,7 +76,8 @@ enum {
 
 /* A strided view of device memory.  data == NULL (or a NULL descriptor
  * pointer) means "absent" for optional arguments.  Strides are in elements;
- * the last dimension must be contiguous (stride 1). */
+ * the last dimension must be contiguous (stride 1).  data is a multiple of the
+ * element size, of q/k/v-like tensors of 16 bytes (BSA_ERR_PARAM_INVALID). */
 typedef struct bsa_tensor {
   void *data;
   int32_t dtype;

@@ -51,6 +51,33 @@ def test_decode_refuses_more_chunks_than_the_line_counts():
     assert _decode_shapes(n, n, 1, 1, 1, 1024, 1) == 161003
 
 
+def test_misaligned_lengths_tables_and_indices_are_refused():
+    """A load from an address that is no multiple of its size faults the GPU."""
+    s = C.make(kvlens=(300, 5), qlens=(3, 1), device="cpu", poison=False)
+    P, lib = C.params(s), bsa.lib()
+    means = torch.zeros(s.B, s.N2, s.NB, s.D, dtype=s.dtype)
+    ix = torch.zeros(s.N2, 2, 4, dtype=torch.uint16)
+    tree = torch.zeros(s.q.shape[0], 1, dtype=torch.int64)
+    lse = torch.zeros(s.q.shape[:2])
+    calls = (  # entry, tensors, place of the params, scalars after it, tensors of whole numbers or 32-bit floats
+        ("bsa_block_means", (s.k, None, s.used, s.table, s.used, means), 5, (), (2, 3, 4)),
+        ("bsa_select_blocks", (s.q, means, s.cu_q, None, s.used, ix), 5, (0, 0), (2, 4, 5)),
+        ("bsa_decode", (s.q, s.k, s.v, ix, tree, s.cu_q, None, s.used, s.table, s.q, lse), 9, (), (3, 4, 5, 7, 8, 10)),
+        ("bsa_fwd", (s.q, s.k, s.v, ix, s.cu_q, None, s.used, s.table, s.q, lse), 8, (), (3, 4, 6, 7, 9)),
+    )
+    for name, tensors, at, extra, whole in calls:
+        def ask(off=None):
+            d = [bsa.describe(t) for t in tensors]
+            if off is not None:
+                d[off].data += 1
+            refs = [None if x is None else ctypes.byref(x) for x in d]
+            n, prm = ctypes.c_size_t(0), P.c()
+            return getattr(lib, name + "_get_workspace")(*refs[:at], ctypes.byref(prm), *extra, *refs[at:], ctypes.byref(n))
+        assert ask() == 0, name
+        for i in whole:
+            assert ask(i) == 161002, (name, i)
+
+
 # ------------------------------------------------- sequences that overlap
 @gpu
 @pytest.mark.parametrize("N1", [2, 32])  # tiles of 16 and of 128 rows
