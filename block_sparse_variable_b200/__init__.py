@@ -7,12 +7,14 @@ the C names; they only marshal torch tensors into ``bsa_tensor``
 descriptors, allocate outputs / workspace with torch when the caller does
 not pass them, and raise ``BsaError`` on a non-OK status.  Every step of
 the computation runs in the library's CUDA kernels: there is no fallback,
-and importing this package fails if the library is missing.
+and importing this package fails if the library is missing.  ``_binding.so``
+is loaded by the first call that needs it.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
 import struct
 from dataclasses import dataclass
@@ -69,9 +71,6 @@ def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           f"`python block_sparse_variable_b200/build.py` (nvcc, sm_100a)")
-    if not os.path.exists(os.path.join(_HERE, "_binding.so")):
-        raise ImportError(f"{_HERE}/_binding.so is missing: build it with "
-                          f"`python block_sparse_variable_b200/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     T = ctypes.POINTER(bsa_tensor)
     Pp = ctypes.POINTER(bsa_params)
@@ -427,7 +426,20 @@ def bsa_fwd_static_workspace(q, k, v, index, params: Params, *, cu_seqlens_q=Non
 # ---------------------------------------------------------- cache operators
 # A decoding step makes these calls for a few microseconds of GPU work each, so
 # the native module _binding describes their tensors and makes the call.
-from . import _binding  # noqa: E402  (needs torch loaded)
+_binding = None
+
+
+def _load_binding():
+    """The native module: only the calls of the cache operators need it, and a
+    host compiler with torch's headers to build it."""
+    global _binding
+    try:
+        _binding = importlib.import_module("._binding", __name__)
+    except ImportError as e:
+        raise ImportError(f"{_HERE}/_binding.so is missing or was built for another torch ({e}): build it with "
+                          f"`python block_sparse_variable_b200/build.py`") from e
+    return _binding
+
 
 _PARAMS = struct.Struct("iiqqqqdiiii")  # bsa_params, padded to its alignment
 assert _PARAMS.size == ctypes.sizeof(bsa_params)
@@ -449,7 +461,7 @@ def _call(name: str, params: Params, tensors, extra, workspace, stream):
     prm = _PARAMS.pack(LAYOUTS[p.q_layout], LAYOUTS[p.kv_layout], p.num_heads, p.num_kv_heads, p.block_shape[0],
                        p.block_shape[1], p.scale, 1 if p.return_lse else 0, 1 if p.causal else 0,
                        1 if p.deterministic else 0, 0)
-    st, sizing, ws = _binding.call(op, fn, fn_ws, prm, tensors, extra, workspace,
+    st, sizing, ws = (_binding or _load_binding()).call(op, fn, fn_ws, prm, tensors, extra, workspace,
                                    None if stream is None else _stream(stream))
     if st:
         raise BsaError(st, name + "_get_workspace" if sizing else name)

@@ -4,6 +4,7 @@ import ctypes
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -26,6 +27,33 @@ def test_line_arithmetic(tmp_path):
     subprocess.check_call([cxx, "-std=c++17", "-Wall", "-Werror", "-I", os.path.join(pkg, "csrc"),
                            os.path.join(os.path.dirname(__file__), "line_check.cpp"), "-o", exe])
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.strip() == "ok"
+
+
+def test_package_works_without_the_native_part_of_the_binding(tmp_path):
+    """A package without _binding.so imports; the passes and the workspace
+    queries work, a call of a cache operator says what is missing."""
+    pkg = os.path.dirname(bsa.LIB_PATH)
+    copy = tmp_path / "block_sparse_variable_b200"
+    copy.mkdir()
+    shutil.copy(os.path.join(pkg, "__init__.py"), copy)
+    os.symlink(bsa.LIB_PATH, copy / "libbsa.so")
+    code = """
+import torch, block_sparse_variable_b200 as bsa
+q = torch.zeros(1, 2, 200, 64, dtype=torch.bfloat16)
+ix = torch.zeros(1, 2, 2, 2, dtype=torch.uint16)
+P = bsa.params_for("BNSD", "BNSD", 2)
+assert bsa.bsa_fwd_get_workspace(q, q, q, ix, P) > 0
+assert bsa.bsa_decode_get_workspace(q, q, q, P) > 0
+try:
+    bsa.bsa_decode(q, q, q, P)
+except ImportError as e:
+    assert "_binding.so" in str(e) and "build.py" in str(e), e
+    print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, PYTHONPATH=str(tmp_path)))
     assert r.returncode == 0, r.stderr
     assert r.stdout.strip() == "ok"
 
