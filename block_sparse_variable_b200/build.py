@@ -15,6 +15,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbsa.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_KEY = os.path.join(BUILD, "binding.txt")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -84,26 +86,43 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
-def build_binding(force: bool = False) -> str:
-    src = os.path.join(CSRC, "binding.cpp")
-    if not force and not _stale_file(BINDING, [src, os.path.join(INCLUDE, "bsa.h")]):
-        return BINDING
+def _binding_cmd(out):
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.dirname(os.path.dirname(nvcc()))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING_SRC, "-o", out,
+            # torch's own libraries: found by name, torch being loaded first
+            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+
+
+def _binding_key():
+    """What the module depends on beside its sources: one torch and one Python."""
+    import torch
+    return f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python {sys.version}\n"
+
+
+def binding_stale() -> bool:
+    if _stale_file(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "bsa.h")]) or not os.path.exists(BINDING_KEY):
+        return True
+    with open(BINDING_KEY) as f:
+        return f.read() != _binding_key()
+
+
+def build_binding(force: bool = False) -> str:
+    if not force and not binding_stale():
+        return BINDING
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o", tmp,
-           # torch's own libraries: found by name, torch being loaded first
-           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    r = subprocess.run(_binding_cmd(tmp), capture_output=True, text=True)
     if r.returncode:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("the host compiler failed for binding.cpp")
     os.replace(tmp, BINDING)
+    with open(BINDING_KEY, "w") as f:
+        f.write(_binding_key())
     return BINDING
 
 

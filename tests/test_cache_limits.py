@@ -58,6 +58,21 @@ except ImportError as e:
     assert r.stdout.strip() == "ok"
 
 
+def test_native_part_is_rebuilt_for_another_torch(monkeypatch, tmp_path):
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("bsa_build", os.path.join(os.path.dirname(bsa.LIB_PATH), "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    key = tmp_path / "binding.txt"
+    monkeypatch.setattr(b, "BINDING_KEY", str(key))
+    monkeypatch.setattr(b, "_stale_file", lambda out, inputs: False)  # the sources are as they were
+    assert b.binding_stale()
+    key.write_text(b._binding_key())
+    assert not b.binding_stale()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert b.binding_stale()
+
+
 def _decode_shapes(T, B, N1, N2, pages, BKV, W):
     """Status of bsa_decode_get_workspace for a paged call of these sizes (no memory behind it)."""
     d = {"q": ((T, N1, 64), BF), "k": ((1, 128, N2, 64), BF), "v": ((1, 128, N2, 64), BF),
