@@ -162,12 +162,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     fence_barrier_init();
   }
+  griddep_wait();
+  // (tensor memory is none of what a block is placed by: taken before the wait,
+  // it could be what a block of the kernel before this one still waits for)
   if (warp == kPvWarp && aligned) {
     tmem_alloc(base + L::kTmemPtr, 512);
     tmem_relinquish();
   }
-  griddep_wait();
-  griddep_launch_next();
   uint32_t len_flags = 0;
   // (the states' memory serves as scratch here; nothing is in static shared
   // memory, so that the tiles start at the aligned window)
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (len_flags) atomicOr(status, len_flags);
   if (!aligned) return;  // the whole block
+  griddep_launch_next();  // the next kernel's blocks find this one's tensor memory taken
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS0 = tmem, tO0 = tmem + 384u;
 

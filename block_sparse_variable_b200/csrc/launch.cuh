@@ -2,12 +2,14 @@
 //
 // Every kernel of a call is launched with programmatic stream serialization:
 // its CTAs may be placed on the SMs while the kernel before it in the stream
-// is still finishing, and wait there (griddep_wait, the first thing each
-// kernel does) until that kernel has completed and its writes are visible.
+// is still finishing, and wait there (griddep_wait, before anything but their
+// own shared memory) until that kernel has completed and its writes are visible.
 // Each kernel then lets the next one be placed (griddep_launch_next), which
 // takes effect once all of its own CTAs have started, so a waiting CTA never
-// holds resources that a CTA of the kernel it waits for still needs.  What
-// this removes is the launch gap between consecutive small kernels.
+// holds threads, registers or shared memory that a CTA of the kernel it waits
+// for still needs.  Tensor memory is taken later, by CTAs that run: every kernel
+// takes it after its wait, so a waiting CTA holds none.  What this removes is
+// the launch gap between consecutive small kernels.
 #pragma once
 
 #include <cuda_runtime.h>

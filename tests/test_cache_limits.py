@@ -73,6 +73,23 @@ def test_native_part_is_rebuilt_for_another_torch(monkeypatch, tmp_path):
     assert b.binding_stale()
 
 
+def test_tensor_memory_is_taken_after_the_wait():
+    """A block that waits for the kernel before it must hold no tensor memory:
+    that kernel's blocks, which may be on the same SM, take theirs while they run."""
+    csrc = os.path.join(os.path.dirname(bsa.LIB_PATH), "csrc")
+    seen = 0
+    for name in sorted(os.listdir(csrc)):
+        if not name.endswith(".cu"):
+            continue
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        for kernel in text.split("__global__")[1:]:
+            if "tmem_alloc(" in kernel:
+                seen += 1
+                assert 0 <= kernel.find("griddep_wait();") < kernel.find("tmem_alloc("), name
+    assert seen >= 4
+
+
 def _decode_shapes(T, B, N1, N2, pages, BKV, W):
     """Status of bsa_decode_get_workspace for a paged call of these sizes (no memory behind it)."""
     d = {"q": ((T, N1, 64), BF), "k": ((1, 128, N2, 64), BF), "v": ((1, 128, N2, 64), BF),
@@ -210,3 +227,26 @@ def test_select_overlapping_sequences_past_32_bit_rows():
     _, ws = bsa.bsa_select_blocks(q, means, P, cu_seqlens_q=cu, seqused_kv=used, index=index)
     assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN | bsa.FLAG_BAD_INDEX
     assert (index.to(torch.int32) == 1).all()
+
+
+@gpu
+def test_passes_and_decode_back_to_back():
+    """Kernels that own an SM's tensor memory after one another in a stream."""
+    s = C.make("TND", qlens=(300, 130), kvlens=(300, 130), N1=8, N2=2, tail_rows=0, poison=False)
+    P = C.params(s, causal=True)
+    k, v = s.k[:430].contiguous(), s.v[:430].contiguous()
+    index = torch.full((s.N2, 5, 3), -1, dtype=torch.int16)
+    for i in range(5):
+        n = i + 1 if i < 3 else i - 2
+        index[:, i, :n] = torch.arange(n, dtype=torch.int16)
+    index = index.cuda().view(torch.uint16)
+    kw = dict(cu_seqlens_q=s.cu_q, cu_seqlens_kv=s.cu_kv)
+    outs = []
+    for _ in range(20):
+        o, l, _ = bsa.bsa_fwd(s.q, k, v, index, P, **kw)
+        outs.append((o, l, bsa.bsa_decode(s.q, k, v, P, index=index, **kw)[:2]))
+    torch.cuda.synchronize()
+    o0, l0, (d0, e0) = outs[0]
+    for o, l, (d, e) in outs:
+        assert torch.equal(o, o0) and torch.equal(l, l0) and torch.equal(d, d0) and torch.equal(e, e0)
+    C.check_decode(s, d0, e0, C.ref_decode(s, (index.to(torch.int32).cpu() & 0xFFFF).tolist(), causal=True))
