@@ -250,3 +250,133 @@ def test_passes_and_decode_back_to_back():
     for o, l, (d, e) in outs:
         assert torch.equal(o, o0) and torch.equal(l, l0) and torch.equal(d, d0) and torch.equal(e, e0)
     C.check_decode(s, d0, e0, C.ref_decode(s, (index.to(torch.int32).cpu() & 0xFFFF).tolist(), causal=True))
+
+
+# ------------------------------------------------------ flags of both kernels
+FEW, TILES = dict(qlens=(1, 1), N1=4), dict(qlens=(40, 21), N1=8)  # rows of a kv head: 2; 160 and 84
+
+
+@gpu
+@pytest.mark.parametrize("kw", [FEW, TILES], ids=["few", "tiles"])
+def test_decode_flags_of_both_kernels(kw):
+    s = C.make(kvlens=(1000, 300), **kw, seed=23)
+    T, ok = s.qlens[0], torch.isfinite
+    n = s.qlens[0] + s.qlens[1]
+    s.table[0, 3] = 1 << 20
+    out, lse, ws = _decode(s, None, None, False)
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_PAGE
+    C.check_decode(s, out, lse, C.ref_decode(s, bad_pages=[(0, 3)]))
+    rows = [[[0, 1, C.NONE], [0, 2, C.NONE]]] * s.N2  # the bad page is not among the selected
+    out, lse, ws = _decode(s, rows, None, False)
+    assert bsa.bsa_read_status(ws) == 0
+    C.check_decode(s, out, lse, C.ref_decode(s, rows))
+    for bad in ([0, 2, 3], [0, 2, 2], [0, 2, 1], [3, 0, 2], [C.NONE, 0, 60000]):  # of one row of one head
+        mixed = [rows[0], [rows[0][0], bad]]
+        out, lse, ws = _decode(s, mixed, None, False)
+        assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_INDEX, bad
+        C.check_decode(s, out, lse, C.ref_decode(s, mixed))
+    out, lse, ws = _decode(s, [[[0, 1, 2]]] * s.N2, None, False)  # no row for the second sequence
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_INDEX
+    assert (out[T:n] == 0).all() and torch.isneginf(lse[T:n]).all() and ok(lse[:T]).all()
+    s.used[0] = s.table.shape[1] * s.page + 1
+    out, lse, ws = _decode(s, None, None, False)
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN
+    assert (out[:T] == 0).all() and torch.isneginf(lse[:T]).all() and ok(lse[T:n]).all()
+
+
+@gpu
+@pytest.mark.parametrize("BKV", [128, 1024])
+@pytest.mark.parametrize("kw", [FEW, TILES], ids=["few", "tiles"])
+def test_decode_messy_index_is_flagged(kw, BKV):
+    """Every row has an entry out of range, some behind all that are taken."""
+    s = C.make(kvlens=(9000, 700), BKV=BKV, **kw, seed=29)
+    rows = C.random_index(s, 40, s.N2, messy=True)
+    out, lse, ws = _decode(s, rows, None, True)
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_INDEX
+    C.check_decode(s, out, lse, C.ref_decode(s, rows, causal=True))
+    # a long valid row and one bad entry at its end
+    nk = [-(-n // BKV) for n in s.kvlens]
+    full = [[list(range(n)) + [C.NONE] * (80 - n) for n in nk] for _ in range(s.N2)]
+    _, _, ws = _decode(s, full, None, True)
+    assert bsa.bsa_read_status(ws) == 0
+    full[-1][0][79] = nk[0]
+    out, lse, ws = _decode(s, full, None, True)
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_INDEX
+    C.check_decode(s, out, lse, C.ref_decode(s, causal=True))
+
+
+# ---------------------------------------------------------- many sequences
+@gpu
+@pytest.mark.parametrize("most", [3, 500])  # rows that stream their own means, tiles
+@pytest.mark.parametrize("rows", ["group", "query"])
+def test_select_many_sequences(most, rows):
+    """More sequences than threads of a block, some of them empty."""
+    g = torch.Generator().manual_seed(41)
+    B = 600
+    qlens = torch.randint(0, most + 1, (B,), generator=g)
+    kvlens = torch.randint(0, 1500, (B,), generator=g)
+    if most > 3:
+        qlens += 150
+    qlens[::7] = 0
+    kvlens[::11] = 0
+    s = C.make(kvlens=kvlens.tolist(), qlens=qlens.tolist(), N1=4, N2=2, D=64, seed=42, poison=False)
+    R = sum(-(-n // s.BQ) for n in s.qlens)
+    assert (R <= 2 * B) == (most == 3)
+    means = torch.randn(s.B, s.N2, s.NB, s.D, generator=s.g).to(s.dtype).cuda()
+    index, ws = _select(s, means, dict(W=4, rows=rows, sink=1))
+    assert bsa.bsa_read_status(ws) == 0
+    assert torch.equal(_as_rows(s, index), C.ref_select(s, means, 4, rows, sink=1).int())
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["causal", "tree", "index"])
+def test_decode_tiles_of_many_sequences(kind):
+    """More sequences than threads of a block, through the 128-row tiles."""
+    g = torch.Generator().manual_seed(43)
+    B = 420
+    qlens = torch.randint(0, 7, (B,), generator=g).tolist()
+    kvlens = torch.randint(0, 300, (B,), generator=g).tolist()
+    s = C.make(kvlens=kvlens, qlens=qlens, N1=8, N2=1, D=64, seed=44)
+    tree = torch.cat([C.random_tree(T, 1, s.g) for T in qlens]) if kind == "tree" else None
+    rows = C.random_index(s, 2, 1) if kind == "index" else None
+    out, lse, ws = _decode(s, rows, tree, kind == "causal")
+    assert bsa.bsa_read_status(ws) == 0
+    C.check_decode(s, out, lse, C.ref_decode(s, rows, tree, kind == "causal"))
+
+
+# --------------------------------------------- rows of more than 1024 blocks
+def _wide(D, dtype, seed, T=(1, 130)):
+    s = C.make(qlens=T, kvlens=(200, 200), N1=4, N2=2, D=D, dtype=dtype, seed=seed, poison=False)
+    s.kvlens = [150000, 131073]  # lengths alone: no cache is read
+    s.used = torch.tensor(s.kvlens, dtype=torch.int32, device="cuda")
+    s.NB = 1172
+    return s
+
+
+@gpu
+@pytest.mark.parametrize("D, dtype", [(128, FP), (64, BF), (128, BF)])
+@pytest.mark.parametrize("W", [7, 400])
+def test_select_wide_rows_with_forced_blocks(D, dtype, W):
+    s = _wide(D, dtype, 51)
+    means = torch.randn(s.B, s.N2, s.NB, D, generator=s.g).to(dtype).cuda()
+    kw = dict(W=W, sink=3, local=2)
+    index, ws = _select(s, means, kw)
+    assert bsa.bsa_read_status(ws) == 0
+    assert torch.equal(_as_rows(s, index), C.ref_select(s, means, W, "group", sink=3, local=2).int())
+
+
+@gpu
+@pytest.mark.parametrize("D, dtype", [(128, FP), (64, BF)])
+@pytest.mark.parametrize("W", [7, 400])
+def test_select_wide_rows_with_ties_beside_forced_blocks(D, dtype, W):
+    """Equal means: hundreds of blocks are scored again, next to forced ones."""
+    s = _wide(D, dtype, 52)
+    for x in s.qd:
+        x.copy_(x.sign())
+    s.q = torch.cat(s.qd).cuda()
+    means = torch.randn(s.B, s.N2, 1, D, generator=s.g).expand(s.B, s.N2, s.NB, D).clone()
+    means[:, :, ::9] = torch.randn(s.B, s.N2, 1, D, generator=s.g)
+    means = means.to(dtype).cuda()
+    index, ws = _select(s, means, dict(W=W, sink=3, local=2))
+    assert bsa.bsa_read_status(ws) == 0
+    assert torch.equal(_as_rows(s, index), C.ref_select(s, means, W, "group", sink=3, local=2).int())
