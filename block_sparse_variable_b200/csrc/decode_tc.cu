@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (wg == 0 && p.lse)
             p.lse[qb * p.l_sb + int64_t(row) * p.l_st + int64_t(head) * p.l_sh] =
-                some ? (mx + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+                some ? (mx + log2f(lsum)) * 0.6931471805599453f : -INFINITY;
         } else {
           // four columns of all rows side by side: a warp's stores are contiguous
           float4 *dst = reinterpret_cast<float4 *>(p.part_o) + (int64_t(slot) * (D / 4) + wg * (D / 8)) * kTile + r;

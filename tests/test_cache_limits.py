@@ -380,3 +380,27 @@ def test_select_wide_rows_with_ties_beside_forced_blocks(D, dtype, W):
     index, ws = _select(s, means, dict(W=W, sink=3, local=2))
     assert bsa.bsa_read_status(ws) == 0
     assert torch.equal(_as_rows(s, index), C.ref_select(s, means, W, "group", sink=3, local=2).int())
+
+
+# ---------------------------------------------------------------- accuracy
+@gpu
+@pytest.mark.parametrize("T", [2, 40])  # tiles of 16 and of 128 rows
+def test_decode_lse_of_a_dominant_key(T):
+    """Two keys with scores 0 and -x: lse = log(1 + e^-x), small against 1.  The
+    sum 1 + e^-x is rounded once (2^-24), e^-x is off by 2^-21 of itself
+    (exponential) and x 2^-22 (products with log2 e in fp32), and the logarithm
+    and its two products by 4 steps of the result."""
+    D, N1 = 64, 8
+    s = C.make(kvlens=(2,), qlens=(T,), N1=N1, N2=1, D=D, tail_rows=0, seed=61)
+    s.k[s.table[0, 0].item(), :2] = 0
+    s.k[s.table[0, 0].item(), 1, :, 0] = 1
+    x = torch.linspace(3, 12, T * N1).view(T, N1).to(BF)
+    s.q.zero_()
+    s.q[..., 0] = -x.cuda()
+    _, lse, _ = bsa.bsa_decode(s.q, s.k, s.v, C.params(s, scale=1.0), cu_seqlens_q=s.cu_q, **C.where(s))
+    x = x.double()
+    e = torch.exp(-x)
+    want = torch.log1p(e)
+    tol = 2.0 ** -24 + e * (2.0 ** -21 + x * 2.0 ** -22) + 4 * 2.0 ** -24 * want
+    d = (lse.double().cpu() - want).abs()
+    assert (d <= tol).all(), float((d / tol).max())
