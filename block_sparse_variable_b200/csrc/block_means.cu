@@ -38,7 +38,8 @@ __device__ void check_inputs(const MeansProblem &p) {
       const int b = int(id / runs), run = int(id % runs);
       uint32_t ignore = 0;
       const KvBatch kb = kv_batch(p.kv, b, ignore);
-      const int used = (kb.kvlen + p.kv.page_size - 1) / p.kv.page_size;
+      const int covered = int(min(int64_t(kb.kvlen), int64_t(p.NB) * p.kv.BKV));  // by blocks that are written
+      const int used = (covered + p.kv.page_size - 1) / p.kv.page_size;
       const int first = p.first_kv ? max(p.first_kv[b], 0) / p.kv.BKV * p.kv.BKV / p.kv.page_size : 0;
       const int x0 = first + run * kRun, n = min(kRun, used - x0);
       const int32_t *row = p.kv.table + int64_t(b) * p.kv.bt_s0 + x0;

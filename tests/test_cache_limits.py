@@ -404,3 +404,21 @@ def test_decode_lse_of_a_dominant_key(T):
     tol = 2.0 ** -24 + e * (2.0 ** -21 + x * 2.0 ** -22) + 4 * 2.0 ** -24 * want
     d = (lse.double().cpu() - want).abs()
     assert (d <= tol).all(), float((d / tol).max())
+
+
+@gpu
+def test_means_flag_only_pages_of_blocks_that_are_written():
+    """A bad page behind the last block that the means have room for."""
+    s = C.make(kvlens=(600, 500), qlens=(1, 1))
+    s.table[0, 4] = -1
+    small = torch.zeros(s.B, s.N2, 3, s.D, dtype=s.dtype, device="cuda")
+    _, ws = bsa.bsa_block_means(s.k, C.params(s), **C.where(s), means=small)
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN  # blocks left out, no page
+    ref = C.ref_means(s)
+    for b in range(2):
+        m, mag = ref[b]
+        d = (small[b].double().cpu() - m[:, :3]).abs()
+        assert (d <= C.half_step(s.dtype) * m[:, :3].abs() + 2.0 ** -16 * mag[:, :3]).all()
+    s.table[0, 2] = -1
+    _, ws = bsa.bsa_block_means(s.k, C.params(s), **C.where(s), means=small)
+    assert bsa.bsa_read_status(ws) == bsa.FLAG_BAD_SEQLEN | bsa.FLAG_BAD_PAGE
