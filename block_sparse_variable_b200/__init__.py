@@ -494,7 +494,11 @@ def bsa_block_means(k, params: Params, *, cu_seqlens_kv=None, seqused_kv=None, b
                     first_kv=None, means=None, workspace=None, stream=None):
     """Means of the keys of every kv block (from token first_kv[b] on), into
     `means` [B, N2, NB, D].  Without `means` a zeroed tensor is made with room
-    for every block the cache can hold.  Returns (means, workspace)."""
+    for every block the cache can hold: for each sequence the tokens of the whole
+    packed tensor (TND) or of a full row of the block table.  Where that is far
+    more than the longest sequence has, pass `means` with less room: the
+    workspace and the time of bsa_select_blocks go by it.  Returns (means,
+    workspace)."""
     if means is None:
         N2, bkv = params.num_kv_heads or params.num_heads, params.block_shape[1]
         if params.kv_layout == "TND":

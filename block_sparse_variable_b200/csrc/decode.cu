@@ -29,7 +29,10 @@ constexpr int kStages = 3;
 // taken; above, the tensor core kernel with 128-row tiles.  (16 sequences of
 // 2048 to 16384 tokens, 8 kv heads: 16 rows 113 us here; 20 rows, two tiles,
 // 202 here and 121 there; 32 rows 206 and 120.  One sequence of 16384 tokens,
-// 20 rows: 37 and 35; of 1500 tokens: 18.6 and 19.4.)
+// 20 rows: 37 and 35; of 1500 tokens: 18.6 and 19.4.)  The mean decides for a
+// mixed batch too: 128 sequences of 4096 tokens, 4 heads a group, 12 rows in the
+// mean, 127 of them with a single token and one with 256: 409 us here, 368 there;
+// one with 64: 334 and 347; all with one: 318 and 327.
 constexpr int kFewRows = 16;
 
 template <int D>

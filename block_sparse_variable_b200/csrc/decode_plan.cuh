@@ -5,16 +5,18 @@
 // query tokens, token-major: they read the same keys) against the kv tokens
 // it sees, cut into chunks.  The chunks of all units form one line, ordered
 // by sequence, head, tile, and block c of G takes the c-th G-th of it: every
-// block has the same number of chunks (within one) whatever the lengths
-// are.  A unit that lies within one block is finished there; the parts of
-// one that does not go to the workspace and a second kernel joins them.  A
-// block starts at most one part at its beginning and one at its end, hence
-// two slots each.
+// block has the same number of chunks (within one).  A unit that lies within
+// one block is finished there; the parts of one that does not go to the
+// workspace and a second kernel joins them.  A block starts at most one part at
+// its beginning and one at its end, hence two slots each.
 // Where a head has several row tiles, `group` blocks side by side take the
 // same chunks for as many tiles, at the same time: the keys and values that
 // one of them brings in serve the others from L2 (32 query heads over 4 kv
 // heads; 16 sequences of 4096 to 16384 tokens, 2 tiles: 134 us without groups,
 // 107 with; 4 of 16384 to 32768, 3 tiles: 105 and 94; 6 tiles: 179 and 154).
+// The line then holds the chunks of whole groups, and where a sequence has
+// fewer tiles than the group, or a rest, the blocks without a tile pass over
+// them: work is even among groups, within a group as the tiles allow.
 #pragma once
 
 #include <limits.h>

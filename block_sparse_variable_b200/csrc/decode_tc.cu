@@ -59,7 +59,11 @@ constexpr int kKWarp = 8, kPvWarp = 9, kVWarp = 10, kSWarp = 11;
 // below 2^8, and the output is rarely rescaled
 constexpr float kSlack = 8.0f;
 // blocks side by side; 16 for 16 tiles are no faster (2 x 256 tokens of 8 heads
-// before 8192: 82 us one by one, 73 to 74 by four, eight or sixteen)
+// before 8192: 82 us one by one, 73 to 74 by four, eight or sixteen; 64 sequences
+// of 65 tokens before 8192: 822 one by one, 748 by the rule below).  The mean
+// number of tokens decides, which a batch of unequal ones pays for: 63 single
+// tokens and a sequence of 4096 before 8192 take 1080 us by the rule and 712 one by
+// one, with a sequence of 1024 357 and 276.
 constexpr int kMostGroup = 8;
 constexpr int kReaders = 11;  // warps that read the chunk lists
 
@@ -545,6 +549,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 a = fma2(make_float2(__uint_as_float(x[32 * h + c]), __uint_as_float(x[32 * h + c + 1])), sc, mm);
             const float2 e = {ex2(a.x), ex2(a.y)};
             ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], e);
+            // rounded to the inputs' type for the product, as in the forward
+            // pass (its sum is not): the product takes one type, and a second
+            // one with the remainders would be half as much again for the
+            // tensor pipe.  Outputs of 32-node trees differ from exact ones by
+            // 0.0023 of their norm, of which the rounding of out makes 0.0017.
             pk[c >> 1] = Pack2<T>::pack(e.x, e.y);
           }
           tmem_st16(tS + uint32_t(16 * h), pk);  // the whole row of S is in registers
@@ -563,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0 && int((kv_it - 1) & 1u) != wg) take_reference();
       if (!ok) break;
       // ---- epilogue: the finished rows, or this block's part of them; group
-      // w writes half of the columns from both groups' outputs
+      // w writes half of the columns, divided by both groups' sums
       if (n > 0) {
         if (!(ok = wait_warp(bar(kBarODone), ended & 1u, abort, status))) break;
         ++ended;

@@ -762,8 +762,6 @@ __device__ __forceinline__ uint16_t *index_row(const SelectProblem &p, int r, in
   return p.index + int64_t(r / p.R) * p.ix_s0 + int64_t(hi) * p.ix_s1 + int64_t(r % p.R) * p.ix_s2;
 }
 
-// A row with 64-bit scores for the blocks whose 32-bit keys lie in [lo, up]:
-// those above are taken, those below are not.
 // Two 16-bit values as doubles times 2^-kDown, by moving their bits: sign,
 // exponent and mantissa go to the top of a double's high word, so subnormals
 // and zeros come out exact too.  (A conversion to 64 bits costs several times
@@ -803,6 +801,8 @@ struct ChooseClose {
   uint16_t id[kClose];
   bool take[kClose];
 };
+// A row with 64-bit scores for the blocks whose 32-bit keys lie in [lo, up]:
+// those above are taken, those below are not.
 template <int D, typename T>
 __device__ __forceinline__ void choose_again(const SelectProblem &p, const SelectAgain &a) {
   constexpr int kLanes = D / 8, kRows = kChooseThreads / kLanes, kLoads = 4;
@@ -1185,6 +1185,10 @@ cudaError_t launch(const SelectProblem &p, cudaStream_t s) {
   // latency.  (32 sequences of 4096 to 16384 tokens, 32 heads, one 128-token
   // block: 34 to 41 us against 78 to 119 by tiles; two blocks 46 to 60 against
   // 65 to 90; three 58 to 79 against 64 to 76; four 70 to 93 against 63 to 79.)
+  // Longer query blocks cost the first kernel more, as every thread block that
+  // streams a part of a row sums its queries: one block of 1024 tokens of 8 and 32
+  // sequences before 16384, 85 against 87 and 121 against 142; two of 8 sequences
+  // 134 against 98.
   if (p.Rg <= 2 * int64_t(p.B)) {
     const int64_t runs = items * (p.NB > 0 ? (p.NB + kFewRun - 1) / kFewRun : 1);
     e = cudaFuncSetAttribute(k_scores_few<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<D>::kBytes);
@@ -1210,9 +1214,11 @@ cudaError_t launch(const SelectProblem &p, cudaStream_t s) {
   }
   if (items == 0) return cudaSuccess;  // the lengths have been checked
   // Up to 1024 blocks a row's keys fit a warp's registers, and no step of its
-  // search waits for a barrier: the whole call takes 53 us against 71 for 64
-  // single tokens before 1023 blocks, and 86 against 333 for a 32768-token
-  // prompt of 24 heads.  Up to 256, eight registers do: 74 us for that prompt.
+  // search waits for a barrier: the whole call takes 48 us against 74 for 64
+  // single tokens before 1024 blocks, and 82 against 317 for a 32768-token
+  // prompt of 24 heads.  Up to 256, eight registers do: 68 us for that prompt.
+  // The room of the means decides, not the blocks that a row has (256 there in
+  // all three), which only the device knows.
   if (p.NB > 1024) return launch_dep(k_choose_wide<D, T>, dim3(unsigned(items)), dim3(kChooseThreads), 0, s, p);
   const dim3 grid(unsigned((items + 3) / 4));
   e = p.NB <= 256 ? launch_dep(k_choose<D, T, 8>, grid, dim3(128), 0, s, p)

@@ -306,6 +306,9 @@ bsa_status bsa_block_means(const bsa_tensor *k, const bsa_tensor *cu_seqlens_kv,
  *             head, or one per group).  Rows that belong to no query block are
  *             left as they were; fewer rows than the lengths need raise
  *             BAD_INDEX.
+ * The workspace holds 8 bytes per index row and block of the means, and the
+ * kernels are chosen by NB: means with room for much more than the longest
+ * sequence cost both.
  * The choice is piecewise constant in q and k, so it has no gradient: bsa_fwd
  * and bsa_bwd with the index are the training pass. */
 bsa_status bsa_select_blocks_get_workspace(const bsa_tensor *q, const bsa_tensor *means,
