@@ -529,7 +529,10 @@ def bsa_select_blocks(q, means, params: Params, *, width=None, index_heads=None,
     made with `width` slots, `index_heads` heads (default: one row per kv
     head) and, for TND queries, `rows` rows (the sum of ceil(qlen /
     block_shape[0]); by default an upper bound, whose last rows are then
-    unused 0xFFFF).  Returns (index, workspace)."""
+    unused 0xFFFF).  The means do not tell how full their last block is: a BNSD
+    cache whose length is no multiple of block_shape[1] gives its lengths in
+    `seqused_kv`, to which the causal mask and local_blocks are aligned.
+    Returns (index, workspace)."""
     if index is None:
         if width is None:
             raise ValueError("bsa_select_blocks: width or index")
